@@ -24,7 +24,9 @@ CONST_DQ, CONST_F32 = 0, 1           # QN_CONST_DQ, QN_CONST_F32
 EXPORTED = ("qn_nf4_sizes", "qn_weight_sizes", "qn_quantize_workspace_size", "nf4_quantize", "nf4_quantize_static_ws", "nf4_dequantize",
             "qlora_workspace_size", "qlora_workspace_check", "qlora_linear_fwd", "qlora_linear_bwd_x",
             "qlora_merge_bf16", "qlora_lora_grads_workspace_size", "qlora_lora_grads", "qlora_linear_fwd_dropout",
-            "qlora_linear_bwd_x_dropout", "qlora_lora_grads_dropout", "qn_status_string",
+            "qlora_linear_bwd_x_dropout", "qlora_lora_grads_dropout", "qn_act8_sizes", "act8_quantize", "act8_dequantize",
+            "swiglu_act8_fwd", "swiglu_act8_bwd", "qn_int4_sizes", "int4_quantize", "int4_dequantize", "int4_linear_fwd",
+            "qn_status_string",
             "qn_last_error", "qn_launch_count", "qn_selftest_wait_timeout")
 
 
@@ -45,6 +47,18 @@ class CWeight(ctypes.Structure):
 class CDropout(ctypes.Structure):
     """qn_lora_dropout (see the header): rate p, generator key and element-index offset."""
     _fields_ = [("p", ctypes.c_float), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64)]
+
+
+class CAct8(ctypes.Structure):
+    """qn_act8 (see the header)."""
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("codes", ctypes.c_void_p),
+                ("absmax", ctypes.c_void_p)]
+
+
+class CInt4(ctypes.Structure):
+    """qn_int4_weight (see the header); zero_point None means 8 for every group."""
+    _fields_ = [("n_out", ctypes.c_int64), ("k_in", ctypes.c_int64), ("group", ctypes.c_int32),
+                ("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("zero_point", ctypes.c_void_p)]
 
 
 def _dropout_struct(dropout) -> CDropout:
@@ -90,6 +104,19 @@ def load(path: str | None = None):
         lib.qlora_linear_bwd_x_dropout.argtypes = lib.qlora_linear_fwd_dropout.argtypes
         lib.qlora_lora_grads_dropout.argtypes = [P, P, i64, i64, i64, P, P, ctypes.c_int, ctypes.c_float, D, P, P,
                                                  P, ctypes.c_size_t, P]
+        A8, I4 = ctypes.POINTER(CAct8), ctypes.POINTER(CInt4)
+        lib.qn_act8_sizes.argtypes = [i64, i64, sz, sz]
+        lib.act8_quantize.argtypes = [P, A8, P]
+        lib.act8_dequantize.argtypes = [A8, P, P]
+        lib.swiglu_act8_fwd.argtypes = [P, P, P, A8, A8, P]
+        lib.swiglu_act8_bwd.argtypes = [A8, A8, P, P, P, A8, P]
+        lib.qn_int4_sizes.argtypes = [i64, i64, ctypes.c_int, sz, sz, sz]
+        lib.int4_quantize.argtypes = [P, I4, P]
+        lib.int4_dequantize.argtypes = [I4, P, P]
+        lib.int4_linear_fwd.argtypes = [I4, P, i64, P, P]
+        for f in ("qn_act8_sizes", "act8_quantize", "act8_dequantize", "swiglu_act8_fwd", "swiglu_act8_bwd",
+                  "qn_int4_sizes", "int4_quantize", "int4_dequantize", "int4_linear_fwd"):
+            getattr(lib, f).restype = st
         for f in ("qlora_merge_bf16", "qlora_lora_grads_workspace_size", "qlora_lora_grads", "qn_nf4_sizes", "qn_quantize_workspace_size", "nf4_quantize", "nf4_quantize_static_ws", "nf4_dequantize",
                   "qlora_workspace_size", "qlora_workspace_check", "qlora_linear_fwd", "qlora_linear_bwd_x",
                   "qlora_linear_fwd_dropout", "qlora_linear_bwd_x_dropout", "qlora_lora_grads_dropout"):
@@ -433,3 +460,227 @@ def qlora_lora_grads(x: torch.Tensor, grad_h: torch.Tensor, A: torch.Tensor, B: 
                                                ctypes.byref(d), _ptr(grad_A), _ptr(grad_B), _ptr(workspace), wsb,
                                                _stream(stream)), "qlora_lora_grads_dropout")
     return grad_A, grad_B
+
+
+# ------------------------------------------------------- activations kept in 8 bits
+# The calls below run on the tensors' device, which has to be the current one, on the current (or the
+# given) stream of it.
+
+def _stream_here(dev: torch.device, stream=None) -> int:
+    """The stream's handle, after checking that `dev` is the device that the library would launch on."""
+    if dev.type != "cuda":
+        raise ValueError(f"the tensors are on {dev}, not on a CUDA device")
+    here = torch.cuda.current_device()
+    if dev.index != here:
+        raise ValueError(f"the tensors are on {dev}, the current device is cuda:{here}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(here)
+    if stream.device_index != here:
+        raise ValueError(f"the stream is one of cuda:{stream.device_index}, the current device is cuda:{here}")
+    return stream.cuda_stream
+
+
+def _expect(t: torch.Tensor, name: str, dtype: torch.dtype, shape, dev: torch.device):
+    """t is a contiguous tensor of this type and shape on `dev`: the library sees only its address."""
+    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+
+
+def _matrix(t: torch.Tensor, name: str):
+    if t.dim() != 2 or t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be a 2-D bf16 tensor, got {t.dtype} of shape {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.shape
+
+
+def act8_sizes(rows: int, cols: int):
+    """(codes, absmax) byte sizes of an activation in 8 bits."""
+    a, b = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(load().qn_act8_sizes(rows, cols, ctypes.byref(a), ctypes.byref(b)), "qn_act8_sizes")
+    return a.value, b.value
+
+
+@dataclasses.dataclass
+class Act8:
+    """An activation in 8 bits (see qn_act8 in include/qlora_nf4.h): a row's 64 consecutive values share an
+    absmax; a value is codes * absmax / 127."""
+    rows: int
+    cols: int
+    codes: torch.Tensor   # int8 [rows, cols]
+    absmax: torch.Tensor  # bfloat16 [rows, cols / 64]
+
+    @staticmethod
+    def empty(rows: int, cols: int, device="cuda") -> "Act8":
+        act8_sizes(rows, cols)  # refuses what the format does not hold
+        return Act8(rows, cols, torch.empty(rows, cols, dtype=torch.int8, device=device),
+                    torch.empty(rows, cols // BLOCK, dtype=torch.bfloat16, device=device))
+
+    def c_struct(self, dev: torch.device, name: str = "Act8") -> CAct8:
+        _expect(self.codes, f"{name}.codes", torch.int8, (self.rows, self.cols), dev)
+        _expect(self.absmax, f"{name}.absmax", torch.bfloat16, (self.rows, self.cols // BLOCK), dev)
+        return CAct8(self.rows, self.cols, self.codes.data_ptr(), self.absmax.data_ptr())
+
+    def nbytes(self) -> int:
+        return self.codes.numel() + 2 * self.absmax.numel()
+
+
+def act8_quantize(x: torch.Tensor, out: Act8 | None = None, stream=None) -> Act8:
+    """An activation (M x k, bf16) in 8 bits, to keep for the backward pass."""
+    M, k = _matrix(x, "x")
+    s = _stream_here(x.device, stream)
+    if out is None:
+        out = Act8.empty(M, k, x.device)
+    elif (out.rows, out.cols) != (M, k):
+        raise ValueError(f"out holds {out.rows} x {out.cols} values, x is {M} x {k}")
+    _check(load().act8_quantize(x.data_ptr(), ctypes.byref(out.c_struct(x.device, "out")), s), "act8_quantize")
+    return out
+
+
+def act8_dequantize(a: Act8, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The bf16 values of an activation in 8 bits."""
+    dev = a.codes.device
+    s = _stream_here(dev, stream)
+    if out is None:
+        out = torch.empty(a.rows, a.cols, dtype=torch.bfloat16, device=dev)
+    else:
+        _expect(out, "out", torch.bfloat16, (a.rows, a.cols), dev)
+    _check(load().act8_dequantize(ctypes.byref(a.c_struct(dev, "a")), out.data_ptr(), s), "act8_dequantize")
+    return out
+
+
+def swiglu_act8_fwd(gate: torch.Tensor, up: torch.Tensor, out: torch.Tensor | None = None, gate8: Act8 | None = None,
+                    up8: Act8 | None = None, stream=None):
+    """(y, gate8, up8): y = silu(gate) * up in bf16, and gate and up in 8 bits for swiglu_act8_bwd."""
+    M, n = _matrix(gate, "gate")
+    dev = gate.device
+    s = _stream_here(dev, stream)
+    _expect(up, "up", torch.bfloat16, (M, n), dev)
+    gate8 = Act8.empty(M, n, dev) if gate8 is None else gate8
+    up8 = Act8.empty(M, n, dev) if up8 is None else up8
+    for a, nm in ((gate8, "gate8"), (up8, "up8")):
+        if (a.rows, a.cols) != (M, n):
+            raise ValueError(f"{nm} holds {a.rows} x {a.cols} values, gate is {M} x {n}")
+    if out is None:
+        out = torch.empty_like(gate)
+    else:
+        _expect(out, "out", torch.bfloat16, (M, n), dev)
+    _check(load().swiglu_act8_fwd(gate.data_ptr(), up.data_ptr(), out.data_ptr(),
+                                  ctypes.byref(gate8.c_struct(dev, "gate8")), ctypes.byref(up8.c_struct(dev, "up8")), s),
+           "swiglu_act8_fwd")
+    return out, gate8, up8
+
+
+def swiglu_act8_bwd(gate8: Act8, up8: Act8, grad_y: torch.Tensor, grad_gate: torch.Tensor | None = None,
+                    grad_up: torch.Tensor | None = None, y8: Act8 | None = None, stream=None, recompute: bool = True):
+    """(grad_gate, grad_up, y8) from what swiglu_act8_fwd kept; y8 is y once more, in 8 bits, the input that the
+    next layer's adapter gradients take (None with recompute=False)."""
+    M, n = gate8.rows, gate8.cols
+    dev = gate8.codes.device
+    s = _stream_here(dev, stream)
+    _expect(grad_y, "grad_y", torch.bfloat16, (M, n), dev)
+    if (up8.rows, up8.cols) != (M, n):
+        raise ValueError(f"up8 holds {up8.rows} x {up8.cols} values, gate8 {M} x {n}")
+    if y8 is None:
+        y8 = Act8.empty(M, n, dev) if recompute else None
+    elif not recompute:
+        raise ValueError("y8 is given with recompute=False")
+    elif (y8.rows, y8.cols) != (M, n):
+        raise ValueError(f"y8 holds {y8.rows} x {y8.cols} values, gate8 {M} x {n}")
+    grads = []
+    for t, nm in ((grad_gate, "grad_gate"), (grad_up, "grad_up")):
+        if t is None:
+            t = torch.empty_like(grad_y)
+        else:
+            _expect(t, nm, torch.bfloat16, (M, n), dev)
+        grads.append(t)
+    _check(load().swiglu_act8_bwd(ctypes.byref(gate8.c_struct(dev, "gate8")), ctypes.byref(up8.c_struct(dev, "up8")),
+                                  grad_y.data_ptr(), grads[0].data_ptr(), grads[1].data_ptr(),
+                                  None if y8 is None else ctypes.byref(y8.c_struct(dev, "y8")), s), "swiglu_act8_bwd")
+    return grads[0], grads[1], y8
+
+
+# ------------------------------------------- 4-bit integer weights with group scales
+
+def int4_sizes(n_out: int, k_in: int, group: int):
+    """(codes, scale, zero_point) byte sizes of a weight in 4-bit integers."""
+    v = [ctypes.c_size_t() for _ in range(3)]
+    _check(load().qn_int4_sizes(n_out, k_in, group, *(ctypes.byref(x) for x in v)), "qn_int4_sizes")
+    return tuple(x.value for x in v)
+
+
+@dataclasses.dataclass
+class Int4Weight:
+    """A weight in 4-bit integers (see qn_int4_weight in include/qlora_nf4.h): scale * (code - zero_point), with a
+    scale and a zero point for each `group` consecutive weights of a row; without zero_point it is 8."""
+    n_out: int
+    k_in: int
+    group: int
+    codes: torch.Tensor                     # uint8 [n_out, k_in / 2]
+    scale: torch.Tensor                     # bfloat16 [n_out, k_in / group]
+    zero_point: torch.Tensor | None = None  # uint8 [n_out, k_in / group], 0..15
+
+    @staticmethod
+    def empty(n_out: int, k_in: int, group: int = 128, zero_point: bool = True, device="cuda") -> "Int4Weight":
+        int4_sizes(n_out, k_in, group)  # refuses what the format does not hold
+        return Int4Weight(n_out, k_in, group, torch.empty(n_out, k_in // 2, dtype=torch.uint8, device=device),
+                          torch.empty(n_out, k_in // group, dtype=torch.bfloat16, device=device),
+                          torch.empty(n_out, k_in // group, dtype=torch.uint8, device=device) if zero_point else None)
+
+    def c_struct(self, dev: torch.device) -> CInt4:
+        if self.group not in (32, 64, 128):
+            raise ValueError(f"group {self.group} is not 32, 64 or 128")
+        groups = (self.n_out, self.k_in // self.group)
+        _expect(self.codes, "codes", torch.uint8, (self.n_out, self.k_in // 2), dev)
+        _expect(self.scale, "scale", torch.bfloat16, groups, dev)
+        z = self.zero_point
+        if z is not None:
+            _expect(z, "zero_point", torch.uint8, groups, dev)
+        return CInt4(self.n_out, self.k_in, self.group, self.codes.data_ptr(), self.scale.data_ptr(),
+                     None if z is None else z.data_ptr())
+
+    def nbytes(self) -> int:
+        return self.codes.numel() + 2 * self.scale.numel() + (0 if self.zero_point is None else self.zero_point.numel())
+
+
+def int4_quantize(W: torch.Tensor, out: Int4Weight | None = None, group: int = 128, zero_point: bool = True,
+                  stream=None) -> Int4Weight:
+    """Quantise a bf16 (n_out x k_in) weight, a merged one for instance, to 4-bit integers; an `out` given keeps its
+    own group and zero points."""
+    n, k = _matrix(W, "W")
+    s = _stream_here(W.device, stream)
+    if out is None:
+        out = Int4Weight.empty(n, k, group, zero_point, W.device)
+    elif (out.n_out, out.k_in) != (n, k):
+        raise ValueError(f"out holds a {out.n_out} x {out.k_in} weight, W is {n} x {k}")
+    _check(load().int4_quantize(W.data_ptr(), ctypes.byref(out.c_struct(W.device)), s), "int4_quantize")
+    return out
+
+
+def int4_dequantize(w: Int4Weight, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    dev = w.codes.device
+    s = _stream_here(dev, stream)
+    if out is None:
+        out = torch.empty(w.n_out, w.k_in, dtype=torch.bfloat16, device=dev)
+    else:
+        _expect(out, "out", torch.bfloat16, (w.n_out, w.k_in), dev)
+    _check(load().int4_dequantize(ctypes.byref(w.c_struct(dev)), out.data_ptr(), s), "int4_dequantize")
+    return out
+
+
+def int4_linear_fwd(w: Int4Weight, x: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """h = dequant(W) x for at most 64 tokens; x is M x k_in, h is M x n_out (bf16)."""
+    dev = x.device
+    s = _stream_here(dev, stream)
+    M = _matrix(x, "x")[0]
+    if x.shape[1] != w.k_in:
+        raise ValueError(f"x has shape {tuple(x.shape)}, the weight takes {w.k_in} features")
+    if out is None:
+        out = torch.empty(M, w.n_out, dtype=torch.bfloat16, device=dev)
+    else:
+        _expect(out, "out", torch.bfloat16, (M, w.n_out), dev)
+    st = load().int4_linear_fwd(ctypes.byref(w.c_struct(dev)), x.data_ptr(), M, out.data_ptr(), s)
+    if st != QN_OK:
+        _check(st, "int4_linear_fwd")
+    return out

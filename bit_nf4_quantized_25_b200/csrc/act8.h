@@ -1,0 +1,27 @@
+// act8.h -- internal launchers of the 8-bit activation checkpoints. Not part of the C ABI.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kernels.h"
+
+namespace qn {
+
+// An activation of `count` values (a multiple of 64) in 8 bits: int8 codes and the bf16 absmax of
+// each 64 consecutive values.
+cudaError_t launch_act8_quantize(const uint16_t *x, int64_t count, int8_t *codes, uint16_t *absmax, cudaStream_t st);
+cudaError_t launch_act8_dequantize(const int8_t *codes, const uint16_t *absmax, int64_t count, uint16_t *x,
+                                   cudaStream_t st);
+
+// y = silu(gate) * up; gate and up also in 8 bits.
+cudaError_t launch_swiglu_act8_fwd(const uint16_t *gate, const uint16_t *up, int64_t count, uint16_t *y,
+                                   int8_t *gate_codes, uint16_t *gate_absmax, int8_t *up_codes, uint16_t *up_absmax,
+                                   cudaStream_t st);
+// The gradients of gate and up from their 8-bit forms; y again in 8 bits when y_codes is not null.
+cudaError_t launch_swiglu_act8_bwd(const int8_t *gate_codes, const uint16_t *gate_absmax, const int8_t *up_codes,
+                                   const uint16_t *up_absmax, const uint16_t *grad_y, int64_t count,
+                                   uint16_t *grad_gate, uint16_t *grad_up, int8_t *y_codes, uint16_t *y_absmax,
+                                   cudaStream_t st);
+
+}  // namespace qn

@@ -7,6 +7,8 @@
 #include <string>
 
 #include "../../include/qlora_nf4.h"
+#include "act8.h"
+#include "int4.h"
 #include "kernels.h"
 
 namespace qn {
@@ -114,6 +116,72 @@ qn_status resolve_dropout(const qn_lora_dropout *d, int r, float sc, DropoutArgs
     *drop = DropoutArgs{d->seed, d->offset, static_cast<uint32_t>(thr)};
     *sc_eff = static_cast<float>(static_cast<double>(sc) / (1.0 - static_cast<double>(d->p)));
     return QN_OK;
+}
+
+bool aligned2(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
+
+// A buffer of an entry point and whether the call writes it.
+struct Span {
+    const void *p;
+    size_t bytes;
+    bool written;
+};
+
+// Whether a written buffer shares a byte with any other.
+template <int N>
+bool overlap(const Span (&s)[N]) {
+    for (int i = 0; i < N; ++i)
+        for (int j = 0; j < N; ++j) {
+            if (i == j || !s[i].written || !s[i].p || !s[j].p || s[i].bytes == 0 || s[j].bytes == 0) continue;
+            const uintptr_t a = reinterpret_cast<uintptr_t>(s[i].p), b = reinterpret_cast<uintptr_t>(s[j].p);
+            if (a < b + s[j].bytes && b < a + s[i].bytes) return true;
+        }
+    return false;
+}
+
+// rows x cols of an activation: both in range, cols a multiple of 64.
+qn_status check_act8_shape(int64_t rows, int64_t cols) {
+    if (rows < 0 || cols < 0) return fail(QN_EINVAL, "negative size rows=%lld cols=%lld", (long long)rows, (long long)cols);
+    if (cols % QN_BLOCK != 0) return fail(QN_ESHAPE, "cols=%lld is not a multiple of %d", (long long)cols, QN_BLOCK);
+    if (rows > kMaxDim || cols > kMaxDim) return fail(QN_ESHAPE, "rows or cols above 2^31-1");
+    if (rows > 0 && cols > 0 && rows * cols >= (int64_t(1) << 42)) return fail(QN_ESHAPE, "more than 2^42 values");
+    return QN_OK;
+}
+
+qn_status check_act8(const qn_act8 *a, const char *name) {
+    if (!a) return fail(QN_EINVAL, "null %s", name);
+    qn_status s = check_act8_shape(a->rows, a->cols);
+    if (s != QN_OK || a->rows == 0 || a->cols == 0) return s;
+    if (!a->codes || !a->absmax) return fail(QN_EINVAL, "null buffer in %s", name);
+    if (!aligned16(a->codes) || !aligned2(a->absmax))
+        return fail(QN_EALIGN, "%s: codes not 16-byte or absmax not 2-byte aligned", name);
+    return QN_OK;
+}
+
+size_t act8_values(const qn_act8 *a) { return static_cast<size_t>(a->rows) * static_cast<size_t>(a->cols); }
+size_t act8_blocks(const qn_act8 *a) { return act8_values(a) / QN_BLOCK; }
+
+qn_status check_int4_shape(int64_t n, int64_t k, int group) {
+    if (group != 32 && group != 64 && group != 128) return fail(QN_EINVAL, "group=%d is not 32, 64 or 128", group);
+    qn_status s = check_shape(n, k);
+    if (s != QN_OK) return s;
+    if (k % group != 0) return fail(QN_ESHAPE, "k_in=%lld is not a multiple of group=%d", (long long)k, group);
+    if (n > 0 && k > 0 && n * k >= (int64_t(1) << 42)) return fail(QN_ESHAPE, "more than 2^42 weights");
+    return QN_OK;
+}
+
+qn_status check_int4(const qn_int4_weight *w) {
+    if (!w) return fail(QN_EINVAL, "null weight struct");
+    qn_status s = check_int4_shape(w->n_out, w->k_in, w->group);
+    if (s != QN_OK || w->n_out == 0 || w->k_in == 0) return s;
+    if (!w->codes || !w->scale) return fail(QN_EINVAL, "null pointer in the quantised weight");
+    if (!aligned16(w->codes) || !aligned2(w->scale))
+        return fail(QN_EALIGN, "codes not 16-byte or scale not 2-byte aligned");
+    return QN_OK;
+}
+
+Int4View view(const qn_int4_weight *w) {
+    return Int4View{w->n_out, w->k_in, w->group, w->codes, w->scale, w->zero_point};
 }
 
 }  // namespace
@@ -433,6 +501,184 @@ qn_status qlora_linear_bwd_x_dropout(const qn_nf4_weight *w, const void *grad_h,
         cudaError_t e = launch_lora_down(gp, M, w->n_out, Bp, 1, r, r, sc, u, RT, st);
         if (e == cudaSuccess) e = launch_adapter_up_masked(u, M, RT, Ap, r, w->k_in, drop, xp, st);
         if (e != cudaSuccess) return cuda_status(e, "qlora_linear_bwd_x");
+    }
+    return cuda_status(cudaSuccess, "");
+}
+
+// ------------------------------------------------------------- 8-bit activations
+
+qn_status qn_act8_sizes(int64_t rows, int64_t cols, size_t *codes_bytes, size_t *absmax_bytes) {
+    if (!codes_bytes || !absmax_bytes) return fail(QN_EINVAL, "null output pointer");
+    qn_status s = check_act8_shape(rows, cols);
+    if (s != QN_OK) return s;
+    *codes_bytes = static_cast<size_t>(rows * cols);
+    *absmax_bytes = 2 * static_cast<size_t>(rows * cols / QN_BLOCK);
+    g_err.clear();
+    return QN_OK;
+}
+
+// x <-> a: the checks of both directions.
+static qn_status check_act8_pair(const qn_act8 *a, const void *x, bool write_x) {
+    qn_status s = check_act8(a, "the 8-bit activation");
+    if (s != QN_OK || a->rows == 0 || a->cols == 0) return s;
+    if (!x) return fail(QN_EINVAL, "null activation pointer");
+    if (!aligned16(x)) return fail(QN_EALIGN, "activation not 16-byte aligned");
+    const Span sp[] = {{x, 2 * act8_values(a), write_x},
+                       {a->codes, act8_values(a), !write_x},
+                       {a->absmax, 2 * act8_blocks(a), !write_x}};
+    if (overlap(sp)) return fail(QN_EINVAL, "an output overlaps another buffer");
+    return QN_OK;
+}
+
+qn_status act8_quantize(const void *x, const qn_act8 *out, void *stream) {
+    qn_status s = check_act8_pair(out, x, false);
+    if (s != QN_OK) return s;
+    if (out->rows == 0 || out->cols == 0) return QN_OK;
+    return cuda_status(launch_act8_quantize(static_cast<const uint16_t *>(x), out->rows * out->cols, out->codes,
+                                            out->absmax, static_cast<cudaStream_t>(stream)),
+                       "act8_quantize");
+}
+
+qn_status act8_dequantize(const qn_act8 *a, void *x_out, void *stream) {
+    qn_status s = check_act8_pair(a, x_out, true);
+    if (s != QN_OK) return s;
+    if (a->rows == 0 || a->cols == 0) return QN_OK;
+    return cuda_status(launch_act8_dequantize(a->codes, a->absmax, a->rows * a->cols, static_cast<uint16_t *>(x_out),
+                                              static_cast<cudaStream_t>(stream)),
+                       "act8_dequantize");
+}
+
+static qn_status check_swiglu(const qn_act8 *gate8, const qn_act8 *up8, const qn_act8 *y8) {
+    qn_status s = check_act8(gate8, "gate8");
+    if (s != QN_OK) return s;
+    s = check_act8(up8, "up8");
+    if (s != QN_OK) return s;
+    if (up8->rows != gate8->rows || up8->cols != gate8->cols) return fail(QN_ESHAPE, "gate8 and up8 differ in shape");
+    if (!y8) return QN_OK;
+    s = check_act8(y8, "y8");
+    if (s != QN_OK) return s;
+    if (y8->rows != gate8->rows || y8->cols != gate8->cols) return fail(QN_ESHAPE, "y8 and gate8 differ in shape");
+    return QN_OK;
+}
+
+qn_status swiglu_act8_fwd(const void *gate, const void *up, void *y, const qn_act8 *gate8, const qn_act8 *up8,
+                          void *stream) {
+    qn_status s = check_swiglu(gate8, up8, nullptr);
+    if (s != QN_OK) return s;
+    if (gate8->rows == 0 || gate8->cols == 0) return QN_OK;
+    if (!gate || !up || !y) return fail(QN_EINVAL, "null activation pointer");
+    if (!aligned16(gate) || !aligned16(up) || !aligned16(y)) return fail(QN_EALIGN, "gate, up or y not 16-byte aligned");
+    const size_t v = act8_values(gate8), b = act8_blocks(gate8);
+    const Span sp[] = {{gate, 2 * v, false},       {up, 2 * v, false},         {y, 2 * v, true},
+                       {gate8->codes, v, true},    {gate8->absmax, 2 * b, true}, {up8->codes, v, true},
+                       {up8->absmax, 2 * b, true}};
+    if (overlap(sp)) return fail(QN_EINVAL, "an output overlaps another buffer");
+    return cuda_status(launch_swiglu_act8_fwd(static_cast<const uint16_t *>(gate), static_cast<const uint16_t *>(up),
+                                              gate8->rows * gate8->cols, static_cast<uint16_t *>(y), gate8->codes,
+                                              gate8->absmax, up8->codes, up8->absmax,
+                                              static_cast<cudaStream_t>(stream)),
+                       "swiglu_act8_fwd");
+}
+
+qn_status swiglu_act8_bwd(const qn_act8 *gate8, const qn_act8 *up8, const void *grad_y, void *grad_gate,
+                          void *grad_up, const qn_act8 *y8, void *stream) {
+    qn_status s = check_swiglu(gate8, up8, y8);
+    if (s != QN_OK) return s;
+    if (gate8->rows == 0 || gate8->cols == 0) return QN_OK;
+    if (!grad_y || !grad_gate || !grad_up) return fail(QN_EINVAL, "null gradient pointer");
+    if (!aligned16(grad_y) || !aligned16(grad_gate) || !aligned16(grad_up))
+        return fail(QN_EALIGN, "grad_y, grad_gate or grad_up not 16-byte aligned");
+    const size_t v = act8_values(gate8), b = act8_blocks(gate8);
+    const Span sp[] = {{gate8->codes, v, false},
+                       {gate8->absmax, 2 * b, false},
+                       {up8->codes, v, false},
+                       {up8->absmax, 2 * b, false},
+                       {grad_y, 2 * v, false},
+                       {grad_gate, 2 * v, true},
+                       {grad_up, 2 * v, true},
+                       {y8 ? y8->codes : nullptr, v, true},
+                       {y8 ? y8->absmax : nullptr, 2 * b, true}};
+    if (overlap(sp)) return fail(QN_EINVAL, "an output overlaps another buffer");
+    return cuda_status(launch_swiglu_act8_bwd(gate8->codes, gate8->absmax, up8->codes, up8->absmax,
+                                              static_cast<const uint16_t *>(grad_y), gate8->rows * gate8->cols,
+                                              static_cast<uint16_t *>(grad_gate), static_cast<uint16_t *>(grad_up),
+                                              y8 ? y8->codes : nullptr, y8 ? y8->absmax : nullptr,
+                                              static_cast<cudaStream_t>(stream)),
+                       "swiglu_act8_bwd");
+}
+
+// ------------------------------------------------- 4-bit integers with group scales
+
+qn_status qn_int4_sizes(int64_t n_out, int64_t k_in, int group, size_t *codes_bytes, size_t *scale_bytes,
+                        size_t *zero_bytes) {
+    if (!codes_bytes || !scale_bytes || !zero_bytes) return fail(QN_EINVAL, "null output pointer");
+    qn_status s = check_int4_shape(n_out, k_in, group);
+    if (s != QN_OK) return s;
+    *codes_bytes = static_cast<size_t>(n_out * k_in / 2);
+    *zero_bytes = static_cast<size_t>(n_out * (k_in / group));
+    *scale_bytes = 2 * *zero_bytes;
+    g_err.clear();
+    return QN_OK;
+}
+
+// W <-> w: the checks of both directions.
+static qn_status check_int4_pair(const qn_int4_weight *w, const void *W, bool write_W) {
+    qn_status s = check_int4(w);
+    if (s != QN_OK || w->n_out == 0 || w->k_in == 0) return s;
+    if (!W) return fail(QN_EINVAL, "null matrix pointer");
+    if (!aligned16(W)) return fail(QN_EALIGN, "matrix not 16-byte aligned");
+    const size_t v = static_cast<size_t>(w->n_out * w->k_in), gr = v / static_cast<size_t>(w->group);
+    const Span sp[] = {{W, 2 * v, write_W},
+                       {w->codes, v / 2, !write_W},
+                       {w->scale, 2 * gr, !write_W},
+                       {w->zero_point, gr, !write_W}};
+    if (overlap(sp)) return fail(QN_EINVAL, "an output overlaps another buffer");
+    return QN_OK;
+}
+
+qn_status int4_quantize(const void *W, const qn_int4_weight *out, void *stream) {
+    qn_status s = check_int4_pair(out, W, false);
+    if (s != QN_OK) return s;
+    if (out->n_out == 0 || out->k_in == 0) return QN_OK;
+    return cuda_status(launch_int4_quantize(static_cast<const uint16_t *>(W), view(out),
+                                            static_cast<cudaStream_t>(stream)),
+                       "int4_quantize");
+}
+
+qn_status int4_dequantize(const qn_int4_weight *w, void *W_out, void *stream) {
+    qn_status s = check_int4_pair(w, W_out, true);
+    if (s != QN_OK) return s;
+    if (w->n_out == 0 || w->k_in == 0) return QN_OK;
+    return cuda_status(launch_int4_dequantize(view(w), static_cast<uint16_t *>(W_out),
+                                              static_cast<cudaStream_t>(stream)),
+                       "int4_dequantize");
+}
+
+qn_status int4_linear_fwd(const qn_int4_weight *w, const void *x, int64_t M, void *h, void *stream) {
+    qn_status s = check_int4(w);
+    if (s != QN_OK) return s;
+    if (M < 0) return fail(QN_EINVAL, "M=%lld out of range", (long long)M);
+    if (M > kDecodeMaxM) return fail(QN_ESHAPE, "M=%lld is above %d tokens", (long long)M, kDecodeMaxM);
+    if (M == 0 || w->n_out == 0) return QN_OK;
+    if (!h) return fail(QN_EINVAL, "null output pointer");
+    if (!aligned16(h)) return fail(QN_EALIGN, "output not 16-byte aligned");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (w->k_in == 0)
+        return cuda_status(cudaMemsetAsync(h, 0, 2 * static_cast<size_t>(M * w->n_out), st), "int4_linear_fwd");
+    if (!x) return fail(QN_EINVAL, "null activation pointer");
+    if (!aligned16(x)) return fail(QN_EALIGN, "activation not 16-byte aligned");
+    const size_t v = static_cast<size_t>(w->n_out * w->k_in), gr = v / static_cast<size_t>(w->group);
+    const Span sp[] = {{h, 2 * static_cast<size_t>(M * w->n_out), true},
+                       {x, 2 * static_cast<size_t>(M * w->k_in), false},
+                       {w->codes, v / 2, false},
+                       {w->scale, 2 * gr, false},
+                       {w->zero_point, gr, false}};
+    if (overlap(sp)) return fail(QN_EINVAL, "h overlaps another buffer");
+    for (int64_t m0 = 0; m0 < M; m0 += kInt4Tokens) {
+        const int mc = static_cast<int>(M - m0 < kInt4Tokens ? M - m0 : kInt4Tokens);
+        cudaError_t e = launch_int4_linear(view(w), static_cast<const uint16_t *>(x) + m0 * w->k_in, mc,
+                                           static_cast<uint16_t *>(h) + m0 * w->n_out, st);
+        if (e != cudaSuccess) return cuda_status(e, "int4_linear_fwd");
     }
     return cuda_status(cudaSuccess, "");
 }

@@ -329,6 +329,114 @@ qn_status qlora_lora_grads_dropout(const void *x, const void *grad_h, int64_t M,
                                    const void *A, const void *B, int r, float alpha, const qn_lora_dropout *dropout,
                                    float *grad_A, float *grad_B, void *ws, size_t ws_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Activations kept in 8 bits for the backward pass. No counterpart on the pages:
+ * only A and B are trained ("How does QLoRA work for training?" (aivaro.ru) 2), so
+ * what a training step has to keep of a frozen linear layer is its input, for
+ * grad_A and grad_B, and of the MLP between them gate and up. These calls keep
+ * them in 1.03 bytes per value instead of 2.
+ *
+ * A block is 64 consecutive values of a row. It holds a = max |x| (exact, bf16) and
+ * per value the code q = 127 x / a rounded to the nearest integer, halves away
+ * from zero; the value read back is q * s with s = fl32(a / 127), so it is within
+ * a / 254 of x. A block of zeros has a = 0 and codes 0. A block that holds a NaN or
+ * an infinity has a = NaN and codes 0: all its values read back as NaN.
+ *   rows, cols : cols % 64 == 0
+ *   codes      : rows * cols bytes, row-major, 16-byte aligned, -127 .. 127
+ *   absmax     : rows * cols / 64 bf16, row-major, 2-byte aligned */
+typedef struct {
+    int64_t rows;
+    int64_t cols;
+    int8_t *codes;
+    uint16_t *absmax;
+} qn_act8;
+
+/* Byte sizes of the two buffers. Errors: QN_EINVAL (null output pointer, negative
+ * size), QN_ESHAPE (cols % 64 != 0). Host-only. */
+qn_status qn_act8_sizes(int64_t rows, int64_t cols, size_t *codes_bytes, size_t *absmax_bytes);
+
+/* act8_quantize -- x (rows x cols bf16) -> its 8-bit form.
+ * Errors: QN_EINVAL (null pointers, x overlapping the buffers), QN_ESHAPE, QN_EALIGN
+ * (x or codes not 16-byte aligned, absmax not 2-byte aligned), QN_ECUDA. */
+qn_status act8_quantize(const void *x, const qn_act8 *out, void *stream);
+
+/* act8_dequantize -- x_out[e] = bf16_rn(fl32(q_e * s_b)). Errors: as act8_quantize. */
+qn_status act8_dequantize(const qn_act8 *a, void *x_out, void *stream);
+
+/* swiglu_act8_fwd -- the activation of the MLP, y = silu(gate) * up, keeping gate and
+ * up in 8 bits:
+ *   y = bf16_rn(g sigma(g) u), sigma(g) = 1 / (1 + exp(-g)), in fp32 from the bf16 gate
+ *   and up; gate8, up8: their 8-bit forms.
+ * gate, up, y : rows x cols bf16 with gate8's rows and cols; up8 has the same. No
+ * output may overlap another output or an input.
+ * Errors: QN_EINVAL, QN_ESHAPE (cols % 64, gate8 and up8 of different shapes), QN_EALIGN,
+ * QN_ECUDA. */
+qn_status swiglu_act8_fwd(const void *gate, const void *up, void *y, const qn_act8 *gate8, const qn_act8 *up8,
+                          void *stream);
+
+/* swiglu_act8_bwd -- the backward pass of swiglu_act8_fwd from what it kept; g and u are
+ * the values that gate8 and up8 read back:
+ *   grad_gate = bf16_rn(grad_y u sigma(g) (1 + g (1 - sigma(g)))),
+ *   grad_up   = bf16_rn(grad_y g sigma(g)),
+ *   y8        = the 8-bit form of bf16_rn(g sigma(g) u): the input of the layer behind the
+ *               activation, for qlora_lora_grads_act8 (NULL: not wanted).
+ * Shapes, aliasing and errors as swiglu_act8_fwd. */
+qn_status swiglu_act8_bwd(const qn_act8 *gate8, const qn_act8 *up8, const void *grad_y, void *grad_gate,
+                          void *grad_up, const qn_act8 *y8, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * 4-bit integer weights with group scales: what a merged weight (qlora_merge_bf16,
+ * "QLoRA & PEFT family" (ai-reference-codex) 3.6 merge_and_unload: a 16-bit matrix) is
+ * served from. No counterpart on the pages.
+ *
+ * A group is `group` = 32, 64 or 128 consecutive weights of a row; a weight is
+ * s * (q - z) with the group's bf16 scale s >= 0, its zero point z in 0..15 and the
+ * code q in 0..15.
+ *   n_out, k_in : k_in % group == 0 and k_in % 64 == 0
+ *   codes       : n_out*k_in/2 bytes, row-major, the element order of qn_nf4_weight
+ *                 (even elements in the low nibble), 16-byte aligned
+ *   scale       : n_out * k_in/group bf16, row-major, 2-byte aligned
+ *   zero_point  : n_out * k_in/group bytes, row-major, each 0..15 (any other value
+ *                 leaves the results unspecified); NULL: every zero point is 8 */
+typedef struct {
+    int64_t n_out;
+    int64_t k_in;
+    int32_t group;
+    uint8_t *codes;
+    uint16_t *scale;
+    uint8_t *zero_point;
+} qn_int4_weight;
+
+/* Byte sizes of the three buffers (zero_bytes is what a non-NULL zero_point needs).
+ * Errors: QN_EINVAL (null output pointer, negative size, a group that is not 32, 64 or
+ * 128), QN_ESHAPE (k_in not a multiple of group and 64, or sizes above the limits).
+ * Host-only. */
+qn_status qn_int4_sizes(int64_t n_out, int64_t k_in, int group, size_t *codes_bytes, size_t *scale_bytes,
+                        size_t *zero_bytes);
+
+/* int4_quantize -- W (n_out x k_in bf16, finite) -> out, with round = to nearest, halves
+ * away from zero. With out->zero_point: lo = min(0, min w), hi = max(0, max w),
+ * s = bf16_rn(fl32((hi - lo) / 15)), z = clamp(round(-lo / s), 0, 15). Without:
+ * s = bf16_rn(fl32(max |w| / 7)), z = 8. q = clamp(round(w / s) + z, 0, 15). A group
+ * whose s is 0 has z = 0 (8 without zero points) and q = z.
+ * Errors: QN_EINVAL, QN_ESHAPE, QN_EALIGN (W or codes not 16-byte aligned, scale not
+ * 2-byte aligned), QN_ECUDA. */
+qn_status int4_quantize(const void *W, const qn_int4_weight *out, void *stream);
+
+/* int4_dequantize -- W_out[e] = bf16_rn(s * (q_e - z)), at most the largest finite bf16
+ * in size. Errors: as int4_quantize. */
+qn_status int4_dequantize(const qn_int4_weight *w, void *W_out, void *stream);
+
+/* int4_linear_fwd -- h = dequant(W) x for a few tokens (decoding):
+ *   h[m, i] = bf16_rn(sum over the groups of row i of s * sum_k (q - z) x[m, k])
+ *   x : M x k_in bf16, h : M x n_out bf16 (written, must not overlap x), M <= 64.
+ * q - z enters exactly, the sums are fp32. Tokens are taken 16 per launch. For more
+ * tokens than 64 the weight is better expanded once (int4_dequantize) for a matrix
+ * product.
+ * Errors: QN_EINVAL, QN_ESHAPE (shape, M > 64), QN_EALIGN (x, h or codes not 16-byte
+ * aligned, scale not 2-byte aligned), QN_ECUDA. */
+qn_status int4_linear_fwd(const qn_int4_weight *w, const void *x, int64_t M, void *h, void *stream);
+
 /* Static description of a status code. */
 const char *qn_status_string(qn_status s);
 
