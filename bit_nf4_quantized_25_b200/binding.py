@@ -25,7 +25,7 @@ EXPORTED = ("qn_nf4_sizes", "qn_weight_sizes", "qn_quantize_workspace_size", "nf
             "qlora_workspace_size", "qlora_workspace_check", "qlora_linear_fwd", "qlora_linear_bwd_x",
             "qlora_merge_bf16", "qlora_lora_grads_workspace_size", "qlora_lora_grads", "qlora_linear_fwd_dropout",
             "qlora_linear_bwd_x_dropout", "qlora_lora_grads_dropout", "qn_act8_sizes", "act8_quantize", "act8_dequantize",
-            "swiglu_act8_fwd", "swiglu_act8_bwd", "qn_int4_sizes", "int4_quantize", "int4_dequantize", "int4_linear_fwd",
+            "qlora_lora_grads_act8_workspace_size", "qlora_lora_grads_act8", "swiglu_act8_fwd", "swiglu_act8_bwd", "qn_int4_sizes", "int4_quantize", "int4_dequantize", "int4_linear_fwd",
             "qn_status_string",
             "qn_last_error", "qn_launch_count", "qn_selftest_wait_timeout")
 
@@ -108,13 +108,16 @@ def load(path: str | None = None):
         lib.qn_act8_sizes.argtypes = [i64, i64, sz, sz]
         lib.act8_quantize.argtypes = [P, A8, P]
         lib.act8_dequantize.argtypes = [A8, P, P]
+        lib.qlora_lora_grads_act8_workspace_size.argtypes = [i64, ctypes.c_int, sz]
+        lib.qlora_lora_grads_act8.argtypes = [A8, P, i64, P, P, ctypes.c_int, ctypes.c_float, D, P, P, P,
+                                              ctypes.c_size_t, P]
         lib.swiglu_act8_fwd.argtypes = [P, P, P, A8, A8, P]
         lib.swiglu_act8_bwd.argtypes = [A8, A8, P, P, P, A8, P]
         lib.qn_int4_sizes.argtypes = [i64, i64, ctypes.c_int, sz, sz, sz]
         lib.int4_quantize.argtypes = [P, I4, P]
         lib.int4_dequantize.argtypes = [I4, P, P]
         lib.int4_linear_fwd.argtypes = [I4, P, i64, P, P]
-        for f in ("qn_act8_sizes", "act8_quantize", "act8_dequantize", "swiglu_act8_fwd", "swiglu_act8_bwd",
+        for f in ("qlora_lora_grads_act8_workspace_size", "qlora_lora_grads_act8", "qn_act8_sizes", "act8_quantize", "act8_dequantize", "swiglu_act8_fwd", "swiglu_act8_bwd",
                   "qn_int4_sizes", "int4_quantize", "int4_dequantize", "int4_linear_fwd"):
             getattr(lib, f).restype = st
         for f in ("qlora_merge_bf16", "qlora_lora_grads_workspace_size", "qlora_lora_grads", "qn_nf4_sizes", "qn_quantize_workspace_size", "nf4_quantize", "nf4_quantize_static_ws", "nf4_dequantize",
@@ -548,6 +551,46 @@ def act8_dequantize(a: Act8, out: torch.Tensor | None = None, stream=None) -> to
         _expect(out, "out", torch.bfloat16, (a.rows, a.cols), dev)
     _check(load().act8_dequantize(ctypes.byref(a.c_struct(dev, "a")), out.data_ptr(), s), "act8_dequantize")
     return out
+
+
+def lora_grads_act8_workspace_size(M: int, r: int) -> int:
+    v = ctypes.c_size_t()
+    _check(load().qlora_lora_grads_act8_workspace_size(M, r, ctypes.byref(v)), "qlora_lora_grads_act8_workspace_size")
+    return v.value
+
+
+def qlora_lora_grads_act8(x: Act8, grad_h: torch.Tensor, A: torch.Tensor, B: torch.Tensor, alpha: float,
+                          grad_A: torch.Tensor | None = None, grad_B: torch.Tensor | None = None,
+                          workspace: torch.Tensor | None = None, stream=None, dropout=None):
+    """(grad_A (r x k_in), grad_B (n_out x r)) in fp32 for an input x kept in 8 bits and grad_h (M x n_out).
+    dropout = (p, seed, offset): the forward's LoRA-dropout mask."""
+    M, k = x.rows, x.cols
+    n = _matrix(grad_h, "grad_h")[1]
+    r = _matrix(A, "A")[0]
+    dev = grad_h.device
+    s = _stream_here(dev, stream)
+    bf, f32 = torch.bfloat16, torch.float32
+    _expect(grad_h, "grad_h", bf, (M, n), dev)
+    _expect(A, "A", bf, (r, k), dev)
+    _expect(B, "B", bf, (n, r), dev)
+    cx = x.c_struct(dev, "x")
+    if grad_A is None:
+        grad_A = torch.empty(r, k, dtype=f32, device=dev)
+    else:
+        _expect(grad_A, "grad_A", f32, (r, k), dev)
+    if grad_B is None:
+        grad_B = torch.empty(n, r, dtype=f32, device=dev)
+    else:
+        _expect(grad_B, "grad_B", f32, (n, r), dev)
+    if workspace is None:
+        workspace = torch.empty(lora_grads_act8_workspace_size(M, r), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    d = None if dropout is None else ctypes.byref(_dropout_struct(dropout))
+    _check(load().qlora_lora_grads_act8(ctypes.byref(cx), grad_h.data_ptr(), n, A.data_ptr(), B.data_ptr(), r,
+                                        float(alpha), d, grad_A.data_ptr(), grad_B.data_ptr(), workspace.data_ptr(),
+                                        workspace.numel() * workspace.element_size(), s), "qlora_lora_grads_act8")
+    return grad_A, grad_B
 
 
 def swiglu_act8_fwd(gate: torch.Tensor, up: torch.Tensor, out: torch.Tensor | None = None, gate8: Act8 | None = None,

@@ -24,4 +24,11 @@ cudaError_t launch_swiglu_act8_bwd(const int8_t *gate_codes, const uint16_t *gat
                                    uint16_t *grad_gate, uint16_t *grad_up, int8_t *y_codes, uint16_t *y_absmax,
                                    cudaStream_t st);
 
+// Adapter gradients (fp32) with the input in 8 bits: grad_A (r x k), grad_B (n x r); M, n, k > 0. The workspace
+// holds t = x A^T and u = grad_h B in fp32.
+size_t act8_grads_workspace_bytes(int64_t M, int r);
+cudaError_t launch_act8_grads(const int8_t *codes, const uint16_t *absmax, const uint16_t *gh, int64_t M, int64_t n,
+                              int64_t k, const uint16_t *A, const uint16_t *B, int r, float s, const DropoutArgs &drop,
+                              float *grad_A, float *grad_B, void *ws, cudaStream_t st);
+
 }  // namespace qn

@@ -1,0 +1,573 @@
+// act8_grads.cu -- the adapter gradients of a linear layer whose input x was kept in 8 bits (act8.cuh):
+//
+//   t = x A^T, u = grad_h B                    (M x r)
+//   grad_B[n, j] = s sum_m grad_h[m, n] t[m, j]
+//   grad_A[j, k] = s sum_m u[m, j] x[m, k]
+//
+// with x = q a / 127, q the int8 codes and a the absmax of 64 neighbouring features, optionally under the
+// forward's LoRA dropout mask. Nothing of x is written back to memory in 16 bits: an int8 code is exact in
+// bf16, so the codes themselves are the tensor-core operands (mma.sync m16n8k16), and a / 127 is applied
+// in fp32: to the 64-feature partial sums of t, and to u before the second product.
+//
+// Results are fp32 and meant to be as good: t and u are kept in fp32 between the two kernels and enter
+// the second product as two bf16 terms, v = hi + lo, which leaves 2^-17 of v. All sums are fp32 in a fixed
+// order.
+//
+// Two kernels, each reading the codes and grad_h once, straight into registers; the second finds in L2
+// what fits there.
+//   k_down   t and u: a warp has 32 tokens, a CTA 128, a cluster splits the features; the adapter's factors go
+//            through shared memory in pieces of 64 features.
+//   k_outer  the two products over tokens: a warp has 64 columns of x or grad_h and every j, a CTA 256 columns
+//            and two token streams, a cluster splits the tokens. The A operand wants neighbouring tokens of one
+//            column in a register: a lane loads 8 columns of 4 tokens and pairs them with byte permutes.
+#include "act8.cuh"
+#include "act8.h"
+#include "dropout.cuh"
+#include "host_cache.h"
+#include "stream_common.cuh"
+
+namespace qn {
+
+namespace {
+
+struct GradArgs {
+    const int8_t *codes;
+    const uint16_t *absmax;
+    const uint16_t *gh;
+    int64_t M, n, k;
+    const uint16_t *A;  // r x k
+    const uint16_t *B;  // n x r
+    int r;              // all of the rank; this launch takes j0 .. j0 + 8 NT
+    int j0;
+    float s;
+    float *grad_A, *grad_B;
+    float *t, *u;  // fragment order, see frag_index
+    DropoutArgs drop;
+};
+
+// t and u lie in the order in which k_outer's lanes read them: per 16 tokens and 8 columns j 32 lanes
+// x 4 values, lane (g, t) the tokens 4 t .. 4 t + 3 of column g.
+__device__ __forceinline__ int64_t frag_index(int64_t m16, int jt_all, int jt, int lane) {
+    return ((m16 * jt_all + jt) * 32 + lane) * 4;
+}
+
+__device__ __forceinline__ float ld_cluster(const float *p, uint32_t rank) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(stream::mapa(stream::saddr(p), rank)) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+
+// Two int8 codes, in the low bytes of the halves of p (the high bytes may hold anything), as a bf16 pair:
+// 128 + (the low seven bits), less 128 for codes >= 0 and 256 for those below; every step is exact.
+__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t p) {
+    const uint32_t a = (p & 0x007f007fu) | 0x43004300u, c = (p & 0x00800080u) | 0x43004300u;
+    const __nv_bfloat162 d =
+        __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&c));
+    return *reinterpret_cast<const uint32_t *>(&d);
+}
+
+// Codes of dropped elements set to 0: 8 consecutive elements from e0 on.
+__device__ __forceinline__ uint2 drop_codes(uint2 v, const DropoutArgs &d, uint64_t e0) {
+    const uint32_t keep = dropout_keep_bits(d, e0, 8);
+    auto bytes = [](uint32_t b) {  // bit i -> byte i
+        return ((b & 1u) | (b & 2u) << 7 | (b & 4u) << 14 | (b & 8u) << 21) * 0xffu;
+    };
+    return make_uint2(v.x & bytes(keep), v.y & bytes(keep >> 4));
+}
+
+// 8 neighbouring bf16 of a row of grad_h from column c on; zeros past its end. Rows that are not 16-byte
+// aligned (n % 8 != 0) are read element by element.
+template <bool kAligned>
+__device__ __forceinline__ uint4 load_gh(const uint16_t *row, int64_t c, int64_t n) {
+    if constexpr (kAligned) {
+        return c < n ? ld_nc_v4(row + c) : make_uint4(0u, 0u, 0u, 0u);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = c + 2 * i < n ? ld_ro_u16(row + c + 2 * i) : 0u;
+            const uint32_t hi = c + 2 * i + 1 < n ? ld_ro_u16(row + c + 2 * i + 1) : 0u;
+            w[i] = lo | (hi << 16);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// ------------------------------------------------------------------------ t and u
+
+constexpr int kDownWarps = 4;
+constexpr int kDownThreads = 32 * kDownWarps;
+constexpr int kDownTokens = 32 * kDownWarps;
+constexpr int kPiece = 64;       // features per step
+constexpr int kARow = 96;        // bf16 per row of the piece of A: 64 and padding (192 B: two rows' 64-byte
+                                 // reads of a quarter warp fall on different banks)
+
+template <int NT>
+struct DownSmem {
+    static constexpr int kBRow = NT == 1 ? 8 : 8 * NT + 8;  // bf16 per row of the piece of B: an odd number of 16-byte
+                                                            // units, so 8 rows in a row are free of conflicts
+    static constexpr int kPieceBytes = 8 * NT * kARow * 2 > kPiece * kBRow * 2 ? 8 * NT * kARow * 2 : kPiece * kBRow * 2;
+    static constexpr int kRedRow = 8 * NT + 1;
+    static constexpr int kRed = kDownTokens * kRedRow * 4;
+    static constexpr int kBytes = 2 * kPieceBytes > kRed ? 2 * kPieceBytes : kRed;
+};
+
+// The order of the features inside 32 is free as long as both operands agree: lane t has the 8 features
+// 8 t .. 8 t + 7, two for each half of two MMAs. Row c of a piece of B goes where the 8 rows of one 8 x 8
+// matrix of ldmatrix are neighbours.
+__device__ __forceinline__ int b_slot(int c) { return (c & 32) | ((c & 7) << 2) | ((c >> 3) & 3); }
+
+template <int NT, bool kX>
+__device__ __forceinline__ void stage_factor(const GradArgs &p, uint16_t *buf, int64_t c0) {
+    if (kX) {
+        // rows j of A, 64 features each
+        for (int i = threadIdx.x; i < 8 * NT * 8; i += kDownThreads) {
+            const int j = i >> 3, seg = i & 7;
+            const bool ok = p.j0 + j < p.r;
+            const uint16_t *src = ok ? p.A + static_cast<int64_t>(p.j0 + j) * p.k + c0 + 8 * seg : p.A;
+            stream::cp_async16_zfill(stream::saddr(buf + j * kARow + 8 * seg), src, ok ? 16u : 0u);
+        }
+    } else if ((p.r & 7) == 0) {
+        for (int i = threadIdx.x; i < kPiece * NT; i += kDownThreads) {
+            const int c = i / NT, seg = i % NT;
+            const bool ok = c0 + c < p.n && p.j0 + 8 * seg < p.r;
+            const uint16_t *src = ok ? p.B + (c0 + c) * p.r + p.j0 + 8 * seg : p.B;
+            stream::cp_async16_zfill(stream::saddr(buf + b_slot(c) * DownSmem<NT>::kBRow + 8 * seg), src, ok ? 16u : 0u);
+        }
+    } else {
+        for (int i = threadIdx.x; i < kPiece * 8 * NT; i += kDownThreads) {
+            const int c = i / (8 * NT), j = i % (8 * NT);
+            const bool ok = c0 + c < p.n && p.j0 + j < p.r;
+            buf[b_slot(c) * DownSmem<NT>::kBRow + j] = ok ? ld_ro_u16(p.B + (c0 + c) * p.r + p.j0 + j) : 0;
+        }
+    }
+    stream::cp_async_commit();
+}
+
+template <int NT, bool kX, bool kDrop, bool kAligned>
+__device__ __forceinline__ void down(const GradArgs &p, uint8_t *smem, int64_t tile, uint32_t rank, uint32_t ranks) {
+    using S = DownSmem<NT>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    auto buf = [&](int b) { return reinterpret_cast<uint16_t *>(smem + b * S::kPieceBytes); };
+    const int64_t m0 = tile * kDownTokens + 32 * warp;
+    const int64_t width = kX ? p.k : p.n, pieces = (width + kPiece - 1) / kPiece;
+    const int64_t lo = pieces * rank / ranks, hi = pieces * (rank + 1) / ranks;
+    int64_t row[4];  // this lane's tokens: g, g + 8, g + 16, g + 24 of the warp's 32
+    bool live[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        const int64_t m = m0 + g + 8 * h;
+        live[h] = m < p.M;
+        row[h] = live[h] ? m : 0;
+    }
+
+    float acc[2][NT][4];
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) acc[mt][nt][0] = acc[mt][nt][1] = acc[mt][nt][2] = acc[mt][nt][3] = 0.0f;
+
+    uint4 v[2][4];       // grad_h: [32 features][token]
+    uint2 q[2][4];       // codes
+    uint32_t top[4];     // absmax of the piece
+    auto load = [&](int64_t c) {
+        const int64_t c0 = c * kPiece + 8 * t;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            if (kX) {
+                const int8_t *src = p.codes + row[h] * p.k + c0;
+#pragma unroll
+                for (int sub = 0; sub < 2; ++sub) q[sub][h] = live[h] ? ld_nc_v2(src + 32 * sub) : make_uint2(0u, 0u);
+                top[h] = live[h] ? ld_ro_u16(p.absmax + row[h] * (p.k / kBlock) + c) : 0u;
+            } else {
+#pragma unroll
+                for (int sub = 0; sub < 2; ++sub)
+                    v[sub][h] = live[h] ? load_gh<kAligned>(p.gh + row[h] * p.n, c0 + 32 * sub, p.n)
+                                        : make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+    };
+
+    if (lo < hi) {
+        stage_factor<NT, kX>(p, buf(0), lo * kPiece);
+        load(lo);
+    }
+    for (int64_t c = lo; c < hi; ++c) {
+        const int b = static_cast<int>((c - lo) & 1);
+        uint32_t a[2][4][4];  // [32 features][token][pair]
+        float sc[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+#pragma unroll
+            for (int sub = 0; sub < 2; ++sub) {
+                if (kX) {
+                    uint2 w = q[sub][h];
+                    if (kDrop && live[h])
+                        w = drop_codes(w, p.drop, p.drop.offset + static_cast<uint64_t>(row[h] * p.k + c * kPiece + 32 * sub + 8 * t));
+                    a[sub][h][0] = codes_to_bf16(__byte_perm(w.x, 0u, 0x4140));
+                    a[sub][h][1] = codes_to_bf16(__byte_perm(w.x, 0u, 0x4342));
+                    a[sub][h][2] = codes_to_bf16(__byte_perm(w.y, 0u, 0x4140));
+                    a[sub][h][3] = codes_to_bf16(__byte_perm(w.y, 0u, 0x4342));
+                } else {
+                    a[sub][h][0] = v[sub][h].x;
+                    a[sub][h][1] = v[sub][h].y;
+                    a[sub][h][2] = v[sub][h].z;
+                    a[sub][h][3] = v[sub][h].w;
+                }
+            }
+            if (kX) sc[h] = __uint_as_float(top[h] << 16) * (1.0f / 127.0f);
+        }
+        if (c + 1 < hi) {
+            stage_factor<NT, kX>(p, buf(b ^ 1), (c + 1) * kPiece);
+            load(c + 1);
+            stream::cp_async_wait_n<1>();
+        } else {
+            stream::cp_async_wait_n<0>();
+        }
+        __syncthreads();
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float d[2][4];
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[mt][i] = kX ? 0.0f : acc[mt][nt][i];
+#pragma unroll
+            for (int sub = 0; sub < 2; ++sub) {
+                uint32_t f[4];
+                if (kX) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(buf(b) + (8 * nt + g) * kARow + 32 * sub + 8 * t);
+                    f[0] = w.x;
+                    f[1] = w.y;
+                    f[2] = w.z;
+                    f[3] = w.w;
+                } else {
+                    const int i = lane & 7;
+                    const int slot = 32 * sub + (2 * (lane >> 3) + (i & 1)) * 4 + (i >> 1);
+                    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
+                                 : "r"(stream::saddr(buf(b) + slot * S::kBRow + 8 * nt)));
+                }
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt) {
+                    const uint32_t(&x0)[4] = a[sub][2 * mt], (&x1)[4] = a[sub][2 * mt + 1];
+                    mma_16816(d[mt], x0[0], x1[0], x0[1], x1[1], f[0], f[1]);
+                    mma_16816(d[mt], x0[2], x1[2], x0[3], x1[3], f[2], f[3]);
+                }
+            }
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[mt][nt][i] = kX ? __fmaf_rn(sc[2 * mt + (i >> 1)], d[mt][i], acc[mt][nt][i]) : d[mt][i];
+        }
+        __syncthreads();  // the buffer is refilled in the next step
+    }
+
+    // the cluster's partial sums, added in rank order; each rank writes its share of the tile
+    float *red = reinterpret_cast<float *>(smem);
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                red[(32 * warp + 16 * mt + g + 8 * (i >> 1)) * S::kRedRow + 8 * nt + 2 * t + (i & 1)] = acc[mt][nt][i];
+    if (ranks > 1) {
+        stream::cluster_arrive_release();
+        stream::cluster_wait_acquire();
+    } else {
+        __syncthreads();
+    }
+    float *out = kX ? p.t : p.u;
+    const int jt_all = (p.r + 7) / 8, jt0 = p.j0 / 8;
+    constexpr int kAll = kDownTokens / 16 * NT * 128;
+    const int e0 = static_cast<int>(kAll * rank / ranks), e1 = static_cast<int>(kAll * (rank + 1) / ranks);
+    for (int e = e0 + threadIdx.x; e < e1; e += kDownThreads) {
+        const int i = e & 3, l = (e >> 2) & 31, nt = (e >> 7) % NT, m16 = e / (128 * NT);
+        const int64_t mg = tile * (kDownTokens / 16) + m16;
+        if (mg * 16 >= p.M || jt0 + nt >= jt_all) continue;
+        const float *src = red + (16 * m16 + 4 * (l & 3) + i) * S::kRedRow + 8 * nt + (l >> 2);
+        float sum = 0.0f;
+        if (ranks > 1)
+            for (uint32_t k = 0; k < ranks; ++k) sum += ld_cluster(src, k);
+        else
+            sum = *src;
+        out[frag_index(mg, jt_all, jt0 + nt, l) + i] = sum;
+    }
+    if (ranks > 1) {  // no CTA leaves while another reads its sums
+        stream::cluster_arrive_release();
+        stream::cluster_wait_acquire();
+    }
+}
+
+// grid (ranks * token tiles, 2): y = 0 takes u from grad_h, y = 1 t from the codes.
+template <int NT, bool kDrop, bool kAligned>
+__global__ void __launch_bounds__(kDownThreads) k_down(const GradArgs p) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    const uint32_t rank = cluster_rank(), ranks = cluster_size();
+    const int64_t tile = blockIdx.x / ranks;
+    if (blockIdx.y == 0)
+        down<NT, false, false, kAligned>(p, smem, tile, rank, ranks);
+    else
+        down<NT, true, kDrop, true>(p, smem, tile, rank, ranks);
+}
+
+// -------------------------------------------------------------- products over tokens
+
+constexpr int kColWarps = 4;
+constexpr int kTokWarps = 2;
+constexpr int kOutThreads = 32 * kColWarps * kTokWarps;
+constexpr int kOutCols = 64 * kColWarps;
+constexpr int kOutRow = kOutCols + 4;  // floats per row j of the sums in shared memory
+
+// v = hi + lo as bf16 pairs: (v0, v1) and (v2, v3).
+__device__ __forceinline__ void split(const float (&v)[4], uint32_t (&hi)[2], uint32_t (&lo)[2]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        hi[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+        lo[i] = pack_bf16x2(v[2 * i] - bf16_lo(hi[i]), v[2 * i + 1] - bf16_hi(hi[i]));
+    }
+}
+
+template <int NT, bool kX, bool kDrop, bool kAligned>
+__device__ __forceinline__ void outer(const GradArgs &p, float *red, int64_t tile, uint32_t rank, uint32_t ranks) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int cw = warp % kColWarps, tw = warp / kColWarps;
+    const int64_t width = kX ? p.k : p.n;
+    const int64_t col0 = tile * kOutCols + 64 * cw, col = col0 + 8 * g;
+    const int jt_all = (p.r + 7) / 8, jt0 = p.j0 / 8;
+    const float *R = kX ? p.u : p.t;
+    const int64_t tiles16 = (p.M + 15) / 16;
+
+    float acc[4][NT][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) acc[i][nt][0] = acc[i][nt][1] = acc[i][nt][2] = acc[i][nt][3] = 0.0f;
+
+    uint4 v[4];
+    uint2 q[4];
+    uint32_t top[4];
+    auto load = [&](int64_t m16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t m = m16 * 16 + 4 * t + i;
+            if (kX) {
+                q[i] = m < p.M ? ld_nc_v2(p.codes + m * p.k + col) : make_uint2(0u, 0u);
+                top[i] = m < p.M ? ld_ro_u16(p.absmax + m * (p.k / kBlock) + col0 / kBlock) : 0u;
+            } else {
+                v[i] = m < p.M ? load_gh<kAligned>(p.gh + m * p.n, col, p.n) : make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+    };
+
+    const int64_t step = kTokWarps * static_cast<int64_t>(ranks);
+    int64_t m16 = rank * kTokWarps + tw;
+    const bool work = col0 < width;
+    if (work && m16 < tiles16) load(m16);
+    for (; work && m16 < tiles16; m16 += step) {
+        uint32_t a[4][4];  // [pair of columns 8 g + 2 i, + 1][tokens 0 1 | tokens 0 1 of the next column | 2 3 | 2 3]
+        float sc[4];
+        if (kX) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (kDrop && m16 * 16 + 4 * t + i < p.M)
+                    q[i] = drop_codes(q[i], p.drop, p.drop.offset + static_cast<uint64_t>((m16 * 16 + 4 * t + i) * p.k + col));
+                sc[i] = __uint_as_float(top[i] << 16) * (1.0f / 127.0f);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t w0 = i < 2 ? q[0].x : q[0].y, w1 = i < 2 ? q[1].x : q[1].y;
+                const uint32_t w2 = i < 2 ? q[2].x : q[2].y, w3 = i < 2 ? q[3].x : q[3].y;
+                const uint32_t b0 = 2u * (i & 1), b1 = b0 + 1u;
+                a[i][0] = codes_to_bf16(__byte_perm(w0, w1, (4u + b0) << 8 | b0));
+                a[i][1] = codes_to_bf16(__byte_perm(w0, w1, (4u + b1) << 8 | b1));
+                a[i][2] = codes_to_bf16(__byte_perm(w2, w3, (4u + b0) << 8 | b0));
+                a[i][3] = codes_to_bf16(__byte_perm(w2, w3, (4u + b1) << 8 | b1));
+            }
+        } else {
+            const uint32_t w[4][4] = {{v[0].x, v[0].y, v[0].z, v[0].w},
+                                      {v[1].x, v[1].y, v[1].z, v[1].w},
+                                      {v[2].x, v[2].y, v[2].z, v[2].w},
+                                      {v[3].x, v[3].y, v[3].z, v[3].w}};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                a[i][0] = __byte_perm(w[0][i], w[1][i], 0x5410);
+                a[i][1] = __byte_perm(w[0][i], w[1][i], 0x7632);
+                a[i][2] = __byte_perm(w[2][i], w[3][i], 0x5410);
+                a[i][3] = __byte_perm(w[2][i], w[3][i], 0x7632);
+            }
+        }
+        const int64_t cur = m16;
+        if (m16 + step < tiles16) load(m16 + step);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            if (jt0 + nt >= jt_all) break;
+            const float4 f = *reinterpret_cast<const float4 *>(R + frag_index(cur, jt_all, jt0 + nt, lane));
+            float w[4] = {f.x, f.y, f.z, f.w};
+            if (kX) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] *= sc[i];
+            }
+            uint32_t h[2], l[2];
+            split(w, h, l);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma_16816(acc[i][nt], a[i][0], a[i][1], a[i][2], a[i][3], h[0], h[1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma_16816(acc[i][nt], a[i][0], a[i][1], a[i][2], a[i][3], l[0], l[1]);
+        }
+    }
+
+    // the token streams of the CTA, then the cluster's CTAs in rank order
+    auto at = [&](int i, int nt, int e) {
+        return red + (8 * nt + 2 * t + (e & 1)) * kOutRow + 64 * cw + 8 * g + 2 * i + (e >> 1);
+    };
+#pragma unroll
+    for (int w = 0; w < kTokWarps; ++w) {
+        if (tw == w) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) *at(i, nt, e) = w == 0 ? acc[i][nt][e] : *at(i, nt, e) + acc[i][nt][e];
+        }
+        __syncthreads();
+    }
+    if (ranks > 1) {
+        stream::cluster_arrive_release();
+        stream::cluster_wait_acquire();
+    }
+    const int js = p.r - p.j0 < 8 * NT ? p.r - p.j0 : 8 * NT;
+    const int all = js * kOutCols;
+    const int e0 = static_cast<int>(static_cast<int64_t>(all) * rank / ranks);
+    const int e1 = static_cast<int>(static_cast<int64_t>(all) * (rank + 1) / ranks);
+    for (int e = e0 + threadIdx.x; e < e1; e += kOutThreads) {
+        // neighbouring threads: neighbouring columns of grad_A, neighbouring j of grad_B
+        const int j = kX ? e / kOutCols : e % js, c = kX ? e % kOutCols : e / js;
+        const int64_t cc = tile * kOutCols + c;
+        if (cc >= width) continue;
+        const float *src = red + j * kOutRow + c;
+        float sum = 0.0f;
+        if (ranks > 1)
+            for (uint32_t k = 0; k < ranks; ++k) sum += ld_cluster(src, k);
+        else
+            sum = *src;
+        if (kX)
+            p.grad_A[static_cast<int64_t>(p.j0 + j) * p.k + cc] = p.s * sum;
+        else
+            p.grad_B[cc * p.r + p.j0 + j] = p.s * sum;
+    }
+    if (ranks > 1) {
+        stream::cluster_arrive_release();
+        stream::cluster_wait_acquire();
+    }
+}
+
+// Column tiles of grad_h first, then those of the codes.
+template <int NT, bool kDrop, bool kAligned>
+__global__ void __launch_bounds__(kOutThreads) k_outer(const GradArgs p) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    const uint32_t rank = cluster_rank(), ranks = cluster_size();
+    const int64_t tile = blockIdx.x / ranks, tiles_gh = (p.n + kOutCols - 1) / kOutCols;
+    if (tile < tiles_gh)
+        outer<NT, false, false, kAligned>(p, reinterpret_cast<float *>(smem), tile, rank, ranks);
+    else
+        outer<NT, true, kDrop, true>(p, reinterpret_cast<float *>(smem), tile - tiles_gh, rank, ranks);
+}
+
+template <typename K>
+cudaError_t launch_clusters(K kern, dim3 grid, int threads, size_t smem, int ranks, const GradArgs &p, cudaStream_t st) {
+    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kern), smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kern, p);
+    if (e != cudaSuccess) return e;
+    count_launch();
+    return cudaGetLastError();
+}
+
+// CTAs that share a tile: doubled until the grid has `want` CTAs, at most 8 and at most `most`.
+int split_ranks(int64_t tiles, int64_t want, int64_t most) {
+    int s = 1;
+    while (s < 8 && tiles * s < want && 2 * s <= most) s *= 2;
+    return s;
+}
+
+template <int NT, bool kDrop, bool kAligned>
+cudaError_t launch_pass(const GradArgs &p, int sms, cudaStream_t st) {
+    const int64_t tok = (p.M + kDownTokens - 1) / kDownTokens;
+    const int64_t pieces = (p.n > p.k ? p.n : p.k) / kPiece;
+    int ranks = split_ranks(2 * tok, 3 * sms, pieces > 1 ? pieces : 1);
+    if (tok * ranks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    cudaError_t e = launch_clusters(k_down<NT, kDrop, kAligned>, dim3(static_cast<unsigned>(tok * ranks), 2, 1), kDownThreads,
+                                    DownSmem<NT>::kBytes, ranks, p, st);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = (p.n + kOutCols - 1) / kOutCols + (p.k + kOutCols - 1) / kOutCols;
+    ranks = split_ranks(tiles, NT > 4 ? sms : 2 * sms, (p.M + 16 * kTokWarps - 1) / (16 * kTokWarps));
+    if (tiles * ranks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    return launch_clusters(k_outer<NT, kDrop, kAligned>, dim3(static_cast<unsigned>(tiles * ranks), 1, 1), kOutThreads,
+                           static_cast<size_t>(8 * NT) * kOutRow * 4, ranks, p, st);
+}
+
+template <int NT>
+cudaError_t launch_nt(const GradArgs &p, int sms, cudaStream_t st) {
+    const bool drop = p.drop.thr != 0u;
+    if (p.n % 8 == 0) return drop ? launch_pass<NT, true, true>(p, sms, st) : launch_pass<NT, false, true>(p, sms, st);
+    return drop ? launch_pass<NT, true, false>(p, sms, st) : launch_pass<NT, false, false>(p, sms, st);
+}
+
+}  // namespace
+
+size_t act8_grads_workspace_bytes(int64_t M, int r) {
+    const size_t one = static_cast<size_t>((M + 15) / 16) * 16 * static_cast<size_t>((r + 7) / 8 * 8) * sizeof(float);
+    return 2 * ((one + 255) & ~size_t(255));
+}
+
+cudaError_t launch_act8_grads(const int8_t *codes, const uint16_t *absmax, const uint16_t *gh, int64_t M, int64_t n,
+                              int64_t k, const uint16_t *A, const uint16_t *B, int r, float s, const DropoutArgs &drop,
+                              float *grad_A, float *grad_B, void *ws, cudaStream_t st) {
+    int sms = 148;
+    cudaError_t e = device_sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    GradArgs p{codes, absmax, gh, M, n, k, A, B, r, 0, s, grad_A, grad_B, static_cast<float *>(ws), nullptr, drop};
+    p.u = reinterpret_cast<float *>(static_cast<char *>(ws) + act8_grads_workspace_bytes(M, r) / 2);
+    for (p.j0 = 0; p.j0 < r; p.j0 += 64) {
+        const int nt = (r - p.j0 + 7) / 8;
+        if (nt <= 1)
+            e = launch_nt<1>(p, sms, st);
+        else if (nt <= 2)
+            e = launch_nt<2>(p, sms, st);
+        else if (nt <= 4)
+            e = launch_nt<4>(p, sms, st);
+        else
+            e = launch_nt<8>(p, sms, st);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace qn

@@ -607,6 +607,63 @@ qn_status swiglu_act8_bwd(const qn_act8 *gate8, const qn_act8 *up8, const void *
                        "swiglu_act8_bwd");
 }
 
+qn_status qlora_lora_grads_act8_workspace_size(int64_t M, int r, size_t *ws_bytes) {
+    if (!ws_bytes) return fail(QN_EINVAL, "null output pointer");
+    if (M < 0 || M > kMaxDim) return fail(QN_EINVAL, "M=%lld out of range", (long long)M);
+    if (r < 1 || r > QN_MAX_RANK) return fail(QN_EINVAL, "rank r=%d outside [1, %d]", r, QN_MAX_RANK);
+    *ws_bytes = act8_grads_workspace_bytes(M, r);
+    g_err.clear();
+    return QN_OK;
+}
+
+qn_status qlora_lora_grads_act8(const qn_act8 *x, const void *grad_h, int64_t n_out, const void *A, const void *B,
+                                int r, float alpha, const qn_lora_dropout *dropout, float *grad_A, float *grad_B,
+                                void *ws, size_t ws_bytes, void *stream) {
+    qn_status s = check_act8(x, "x");
+    if (s != QN_OK) return s;
+    const int64_t M = x->rows, k = x->cols;
+    s = check_shape(n_out, k);
+    if (s != QN_OK) return s;
+    if (r < 1 || r > QN_MAX_RANK) return fail(QN_EINVAL, "rank r=%d outside [1, %d]", r, QN_MAX_RANK);
+    DropoutArgs drop;
+    float sc = alpha / static_cast<float>(r);
+    s = resolve_dropout(dropout, r, sc, &drop, &sc);
+    if (s != QN_OK) return s;
+    if (!(alpha - alpha == 0.0f)) return fail(QN_EINVAL, "alpha is not finite");
+    const size_t a_bytes = static_cast<size_t>(r) * static_cast<size_t>(k), b_bytes = static_cast<size_t>(r) * static_cast<size_t>(n_out);
+    if ((a_bytes && !grad_A) || (b_bytes && !grad_B)) return fail(QN_EINVAL, "null gradient output");
+    if ((reinterpret_cast<uintptr_t>(grad_A) & 3u) != 0 || (reinterpret_cast<uintptr_t>(grad_B) & 3u) != 0)
+        return fail(QN_EALIGN, "grad_A or grad_B not 4-byte aligned");
+    const bool empty = M == 0 || k == 0 || n_out == 0;
+    const size_t need = act8_grads_workspace_bytes(M, r);
+    if (!empty) {
+        if (!A || !B) return fail(QN_EINVAL, "null adapter pointer with r=%d", r);
+        if (!grad_h) return fail(QN_EINVAL, "null activation pointer");
+        if (!aligned16(A) || !aligned16(B) || !aligned16(grad_h)) return fail(QN_EALIGN, "A, B or grad_h not 16-byte aligned");
+        if (!ws || ws_bytes < need) return fail(QN_EWORKSPACE, "adapter-gradient workspace needs %zu bytes", need);
+        if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return fail(QN_EALIGN, "workspace not 256-byte aligned");
+    }
+    const Span sp[] = {{x->codes, act8_values(x), false},
+                       {x->absmax, 2 * act8_blocks(x), false},
+                       {grad_h, 2 * static_cast<size_t>(M) * static_cast<size_t>(n_out), false},
+                       {A, 2 * a_bytes, false},
+                       {B, 2 * b_bytes, false},
+                       {grad_A, 4 * a_bytes, true},
+                       {grad_B, 4 * b_bytes, true},
+                       {empty ? nullptr : ws, need, true}};
+    if (overlap(sp)) return fail(QN_EINVAL, "an output overlaps another buffer");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (empty) {  // no token, or one side without features: what gradients there are, are zero
+        cudaError_t e = a_bytes ? cudaMemsetAsync(grad_A, 0, 4 * a_bytes, st) : cudaSuccess;
+        if (e == cudaSuccess && b_bytes) e = cudaMemsetAsync(grad_B, 0, 4 * b_bytes, st);
+        return cuda_status(e, "qlora_lora_grads_act8");
+    }
+    return cuda_status(launch_act8_grads(x->codes, x->absmax, static_cast<const uint16_t *>(grad_h), M, n_out, k,
+                                         static_cast<const uint16_t *>(A), static_cast<const uint16_t *>(B), r, sc,
+                                         drop, grad_A, grad_B, ws, st),
+                       "qlora_lora_grads_act8");
+}
+
 // ------------------------------------------------- 4-bit integers with group scales
 
 qn_status qn_int4_sizes(int64_t n_out, int64_t k_in, int group, size_t *codes_bytes, size_t *scale_bytes,

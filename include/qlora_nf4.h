@@ -363,6 +363,28 @@ qn_status act8_quantize(const void *x, const qn_act8 *out, void *stream);
 /* act8_dequantize -- x_out[e] = bf16_rn(fl32(q_e * s_b)). Errors: as act8_quantize. */
 qn_status act8_dequantize(const qn_act8 *a, void *x_out, void *stream);
 
+/* Workspace bytes qlora_lora_grads_act8 needs for M tokens and rank r (1..256).
+ * Host-only. The workspace's contents on entry do not matter. */
+qn_status qlora_lora_grads_act8_workspace_size(int64_t M, int r, size_t *ws_bytes);
+
+/* qlora_lora_grads_act8 -- qlora_lora_grads for an input that was kept in 8 bits: the
+ * same gradients, of the values that x reads back (M = x->rows, k_in = x->cols):
+ *   grad_B[n, j] = s * sum_m grad_h[m,n] t[m,j],  t = x A^T        (n_out x r)
+ *   grad_A[j, k] = s * sum_m u[m,j] x[m,k],       u = grad_h B     (r x k_in)
+ * A, B, grad_h, grad_A, grad_B as there; dropout (NULL: none) as in
+ * qlora_lora_grads_dropout, with x the undropped input. The codes and the bf16
+ * operands enter exactly, t and u with 16 bits, all sums are fp32 in a fixed order:
+ * results are bit-reproducible. A token whose t or u is not finite makes every
+ * gradient that it enters NaN. M, n_out or k_in 0: the gradients are zero.
+ * ws: at least qlora_lora_grads_act8_workspace_size() bytes, 256-byte aligned.
+ * Errors: QN_EINVAL (null pointer, r outside 1..256, alpha not finite, a dropout rate
+ * outside [0, 1), an output that overlaps another buffer), QN_ESHAPE, QN_EALIGN (A, B,
+ * grad_h or the codes not 16-byte, grad_A or grad_B not 4-byte aligned),
+ * QN_EWORKSPACE, QN_ECUDA. */
+qn_status qlora_lora_grads_act8(const qn_act8 *x, const void *grad_h, int64_t n_out, const void *A, const void *B,
+                                int r, float alpha, const qn_lora_dropout *dropout, float *grad_A,
+                                float *grad_B, void *ws, size_t ws_bytes, void *stream);
+
 /* swiglu_act8_fwd -- the activation of the MLP, y = silu(gate) * up, keeping gate and
  * up in 8 bits:
  *   y = bf16_rn(g sigma(g) u), sigma(g) = 1 / (1 + exp(-g)), in fp32 from the bf16 gate

@@ -61,3 +61,11 @@ def int4_values(codes: torch.Tensor, scale: torch.Tensor, zero_point, group: int
     q = int4_unpack(codes).double().reshape(codes.shape[0], -1, group)
     z = 8.0 if zero_point is None else zero_point.double().unsqueeze(-1)
     return ((q - z) * scale.double().unsqueeze(-1)).reshape(codes.shape[0], -1)
+
+
+def lora_grads(x, gh, A, B, s):
+    """(grad_A, grad_B, bounds of both) in 64 bits; the bounds are sums of the sizes of all terms, in units of
+    which the fp32 arithmetic errs."""
+    t, u = x @ A.t(), gh @ B
+    tb, ub = x.abs() @ A.abs().t(), gh.abs() @ B.abs()
+    return s * (u.t() @ x), s * (gh.t() @ t), s * (ub.t() @ x.abs()), s * (gh.abs().t() @ tb)

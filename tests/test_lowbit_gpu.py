@@ -203,6 +203,143 @@ def test_swiglu_nan_block_reaches_the_gradients():
     assert torch.equal(qb.act8_dequantize(y8).isnan(), bad)
 
 
+# ------------------------------------------------------------------- adapter gradients
+
+def check_grads(x8, gh, A, B, alpha, keep=None, dropout=None, **kw):
+    M, n, k, r = gh.shape[0], gh.shape[1], A.shape[1], A.shape[0]
+    ga, gb = qb.qlora_lora_grads_act8(x8, gh, A, B, alpha, dropout=dropout, **kw)
+    x, s = ref.act8_values(x8.codes, x8.absmax), alpha / r
+    if keep is not None:
+        x, s = x * keep, s / (1.0 - dropout[0])
+    wa, wb, sa, sb = ref.lora_grads(x, gh.double(), A.double(), B.double(), s)
+    # In units of the sum of the terms' sizes: t (u) is a chain of fp32 additions, 4 of the tensor core and one fma for
+    # 64 features, and 8 over the cluster (2^-23 each); two bf16 terms leave 2^-16; the products over tokens are a chain
+    # of 2 for 16 tokens, at most M / 16, and 10 over the CTA and cluster (2^-23 each); s and a / 127 2^-23 each.
+    def unit(features):
+        return ((5 * features / 64 + 8) + (2 * M / 16 + 10) + 4) * 2.0 ** -23 + 2.0 ** -16
+    within(ga, wa, sa * unit(n) + 1e-30, "grad_A")
+    within(gb, wb, sb * unit(k) + 1e-30, "grad_B")
+    return ga, gb
+
+
+def grad_inputs(M, n, k, r, seed=0):
+    x8 = qb.act8_quantize(rand(M, k, seed=seed))
+    return x8, rand(M, n, seed=seed + 1), rand(r, k, std=0.01, seed=seed + 2), rand(n, r, std=0.01, seed=seed + 3)
+
+
+@pytest.mark.parametrize("M", [1, 2, 15, 16, 17, 32, 33, 100, 127, 128, 129, 300, 1000])
+def test_grads_tokens(M):
+    check_grads(*grad_inputs(M, 200, 192, 16, seed=M), 32.0)
+
+
+@pytest.mark.parametrize("r", [1, 3, 8, 13, 16, 17, 32, 33, 64, 65, 100, 128, 256])
+def test_grads_ranks(r):
+    check_grads(*grad_inputs(70, 136, 320, r, seed=r), 2.0 * r)
+
+
+@pytest.mark.parametrize("n,k", [(1, 64), (7, 64), (8, 128), (63, 448), (255, 256), (257, 320), (1000, 64 * 21),
+                                 (4096, 4096), (11008, 4096), (4096, 11008), (4097, 64 * 17)])
+def test_grads_shapes(n, k):
+    check_grads(*grad_inputs(150, n, k, 16, seed=n), 32.0)
+
+
+@pytest.mark.parametrize("n,k,r", [(4096, 4096, 16), (1028, 1024, 64), (1031, 1024, 24)])
+def test_grads_long_batches(n, k, r):
+    check_grads(*grad_inputs(4099, n, k, r, seed=n), 32.0)
+
+
+def test_grads_70b_layer():
+    check_grads(*grad_inputs(1030, 28672, 8192, 64, seed=1), 16.0)
+
+
+@pytest.mark.parametrize("offset", [0, 3, 2 ** 33 + 1])
+@pytest.mark.parametrize("r", [4, 40])
+def test_grads_dropout(oracle, offset, r):
+    M, n, k = 37, 50, 192
+    p, seed = 0.25, 1234567890123
+    x8, gh, A, B = grad_inputs(M, n, k, r)
+    keep = torch.from_numpy(oracle.dropout_keep(seed, offset, p, M, k)).to(DEV)
+    assert 0.6 < float(keep.double().mean()) < 0.9
+    ga, gb = check_grads(x8, gh, A, B, 8.0, keep=keep.double(), dropout=(p, seed, offset))
+    plain = qb.qlora_lora_grads_act8(x8, gh, A, B, 8.0)
+    off = qb.qlora_lora_grads_act8(x8, gh, A, B, 8.0, dropout=(0.0, seed, offset))
+    assert all(torch.equal(a, b) for a, b in zip(plain, off)) and not torch.equal(ga, plain[0])
+
+
+def test_grads_agree_with_the_16_bit_entry_point():
+    # an input whose values an 8-bit block holds exactly: the same gradients as from bf16, to that call's own 1e-2
+    M, n, k, r = 200, 320, 256, 16
+    g = torch.Generator(device=DEV)
+    g.manual_seed(0)
+    x = torch.randint(-127, 128, (M, k), device=DEV, generator=g).to(BF)
+    x[:, ::64] = 127.0
+    x8 = qb.act8_quantize(x)
+    assert torch.equal(qb.act8_dequantize(x8), x)
+    _, gh, A, B = grad_inputs(M, n, k, r)
+    for d in (None, (0.1, 7, 2)):
+        for a, b in zip(qb.qlora_lora_grads_act8(x8, gh, A, B, 32.0, dropout=d),
+                        qb.qlora_lora_grads(x, gh, A, B, 32.0, dropout=d)):
+            a, b = a.double(), b.double()
+            within(a, b, 1e-2 * b.abs() + 1e-2 * b.square().mean().sqrt())
+
+
+def test_grads_are_reproducible_and_stay_inside_their_buffers():
+    M, n, k, r = 130, 205, 192, 13
+    x8, gh, A, B = grad_inputs(M, n, k, r)
+    aw, a = guarded(r * k, torch.float32, 7.0)
+    bw, b = guarded(n * r, torch.float32, 7.0)
+    need = qb.lora_grads_act8_workspace_size(M, r)
+    whole = torch.full((need + 512,), 77, dtype=torch.uint8, device=DEV)
+    first = qb.qlora_lora_grads_act8(x8, gh, A, B, 26.0, grad_A=a.view(r, k), grad_B=b.view(n, r),
+                                     workspace=whole[256:256 + need])
+    assert guards_kept(aw, 7.0) and guards_kept(bw, 7.0)
+    assert bool((whole[:256] == 77).all()) and bool((whole[256 + need:] == 77).all())
+    for _ in range(3):
+        again = qb.qlora_lora_grads_act8(x8, gh, A, B, 26.0)
+        assert all(torch.equal(u, v) for u, v in zip(first, again))
+
+
+def test_grads_empty_sides():
+    x8, gh, A, B = grad_inputs(0, 40, 128, 8)
+    ga, gb = qb.qlora_lora_grads_act8(x8, gh, A, B, 8.0)
+    assert int(ga.count_nonzero()) == 0 and int(gb.count_nonzero()) == 0
+    x8, _, A, _ = grad_inputs(5, 40, 128, 8)
+    ga, gb = qb.qlora_lora_grads_act8(x8, rand(5, 0), A, rand(0, 8), 8.0)
+    assert gb.shape == (0, 8) and int(ga.count_nonzero()) == 0
+
+
+def test_grads_nan_block_and_zero_blocks():
+    M, n, k, r = 40, 72, 192, 8
+    x = rand(M, k, seed=1)
+    x[:, 64:128] = 0.0
+    x8 = qb.act8_quantize(x)
+    _, gh, A, B = grad_inputs(M, n, k, r)
+    ga, _ = check_grads(x8, gh, A, B, 8.0)
+    assert int(ga[:, 64:128].count_nonzero()) == 0
+    x[7, 3] = float("nan")
+    ga, gb = qb.qlora_lora_grads_act8(qb.act8_quantize(x), gh, A, B, 8.0)
+    assert bool(gb.isnan().all()) and bool(ga[:, :64].isnan().all()) and not bool(ga[:, 64:].isnan().any())
+
+
+def test_grads_against_differences():
+    # the loss is sum(grad_h * s B A x) over the values read back; moved along one entry of A and of B
+    M, n, k, r = 33, 48, 128, 8
+    x8, gh, A, B = grad_inputs(M, n, k, r)
+    ga, gb = qb.qlora_lora_grads_act8(x8, gh, A, B, 16.0)
+    x, g = ref.act8_values(x8.codes, x8.absmax), gh.double()
+    loss = lambda A, B: float((g * (2.0 * (x @ A.t()) @ B.t())).sum())  # noqa: E731
+    for j, i in ((0, 0), (7, 127), (3, 70)):
+        e = torch.zeros(r, k, dtype=torch.float64, device=DEV)
+        e[j, i] = 1e-3
+        d = (loss(A.double() + e, B.double()) - loss(A.double() - e, B.double())) / 2e-3  # linear in A: exact
+        assert abs(d - float(ga[j, i])) <= 1e-4 * float(ga.abs().max())
+    for i, j in ((0, 0), (47, 7), (20, 3)):
+        e = torch.zeros(n, r, dtype=torch.float64, device=DEV)
+        e[i, j] = 1e-3
+        d = (loss(A.double(), B.double() + e) - loss(A.double(), B.double() - e)) / 2e-3
+        assert abs(d - float(gb[i, j])) <= 1e-4 * float(gb.abs().max())
+
+
 # ------------------------------------------------------------------- 4-bit integers
 
 @pytest.mark.parametrize("n,k", [(1, 128), (3, 384), (17, 1280), (100, 4096), (33, 11008)])
@@ -344,14 +481,16 @@ def test_int4_empty():
 def test_calls_on_another_stream_and_in_a_graph():
     x, gate, up, dy = (rand(9, 640, seed=s) for s in range(4))
     W, xs = rand(96, 640, std=0.02, seed=5), rand(4, 640, seed=6)
+    A, B = rand(8, 640, seed=7), rand(640, 8, seed=8)
 
     def step(stream=None):
         a = qb.act8_quantize(x, stream=stream)
         y, g8, u8 = qb.swiglu_act8_fwd(gate, up, stream=stream)
         gg, gu, y8 = qb.swiglu_act8_bwd(g8, u8, dy, stream=stream)
+        ga, gb = qb.qlora_lora_grads_act8(a, up, A, B, 8.0, stream=stream, dropout=(0.1, 5, 0))
         w = qb.int4_quantize(W, stream=stream)
         h = qb.int4_linear_fwd(w, xs, stream=stream)
-        return (qb.act8_dequantize(a, stream=stream), y, gg, gu, qb.act8_dequantize(y8, stream=stream),
+        return (qb.act8_dequantize(a, stream=stream), y, gg, gu, ga, gb, qb.act8_dequantize(y8, stream=stream),
                 qb.int4_dequantize(w, stream=stream), h)
 
     want = step()
@@ -398,3 +537,54 @@ def test_binding_refusals_on_the_gpu():
     assert e.value.status == qb.QN_ESHAPE
     with pytest.raises(qb.QNError):
         qb.int4_quantize(rand(4, 128), group=48)
+
+
+# ------------------------------------------------------------------ the calls together
+
+def test_a_training_step_then_the_merged_layer_decodes():
+    """One MLP of a frozen 4-bit base: gate, up and down with adapters, forward and backward with what is kept in 8
+    bits, a step on the adapters, the merge, and the merged down projection served from 4-bit integers."""
+    M, d, f, r, alpha, lr = 50, 256, 448, 8, 16.0, 0.5
+    s = alpha / r
+    W = {nm: rand(*sh, std=0.05, seed=i) for i, (nm, sh) in enumerate((("gate", (f, d)), ("up", (f, d)), ("down", (d, f))))}
+    w = {nm: qb.nf4_quantize(v) for nm, v in W.items()}
+    A = {nm: rand(r, v.shape[1], std=0.05, seed=10 + i) for i, (nm, v) in enumerate(W.items())}
+    B = {nm: rand(v.shape[0], r, std=0.05, seed=20 + i) for i, (nm, v) in enumerate(W.items())}
+    x, dy = rand(M, d, seed=30), rand(M, d, seed=31)
+
+    x8 = qb.act8_quantize(x)
+    gate, up = (qb.qlora_linear_fwd(w[nm], x, A[nm], B[nm], alpha) for nm in ("gate", "up"))
+    act, gate8, up8 = qb.swiglu_act8_fwd(gate, up)
+    y = qb.qlora_linear_fwd(w["down"], act, A["down"], B["down"], alpha)
+    d_act = qb.qlora_linear_bwd_x(w["down"], dy, A["down"], B["down"], alpha)
+    d_gate, d_up, act8 = qb.swiglu_act8_bwd(gate8, up8, d_act)
+    grads = {"down": qb.qlora_lora_grads_act8(act8, dy, A["down"], B["down"], alpha),
+             "gate": qb.qlora_lora_grads_act8(x8, d_gate, A["gate"], B["gate"], alpha),
+             "up": qb.qlora_lora_grads_act8(x8, d_up, A["up"], B["up"], alpha)}
+
+    # the same in 64 bits without any rounding of activations
+    D = {nm: qb.nf4_dequantize(w[nm]).double() + s * B[nm].double() @ A[nm].double() for nm in W}
+    g, u = x.double() @ D["gate"].t(), x.double() @ D["up"].t()
+    a = ref.swiglu(g, u)
+    da = dy.double() @ D["down"]
+    dg, du = ref.swiglu_grads(g, u, da)
+    want = {"down": ref.lora_grads(a, dy.double(), A["down"].double(), B["down"].double(), s),
+            "gate": ref.lora_grads(x.double(), dg, A["gate"].double(), B["gate"].double(), s),
+            "up": ref.lora_grads(x.double(), du, A["up"].double(), B["up"].double(), s)}
+    for nm in W:
+        for got, exact in zip(grads[nm], want[nm][:2]):
+            # 8 bits of a block leave at most 1/254 of its largest, near 1 % of the rms; a gradient mixes a few of these
+            assert float((got.double() - exact).norm() / exact.norm()) < 0.05, nm
+    assert float((y.double() - a @ D["down"].t()).norm() / (a @ D["down"].t()).norm()) < 0.03
+
+    for nm in W:
+        A[nm] = (A[nm].float() - lr * grads[nm][0]).to(BF)
+        B[nm] = (B[nm].float() - lr * grads[nm][1]).to(BF)
+    merged = qb.qlora_merge_bf16(w["down"], A["down"], B["down"], alpha)
+    served = qb.int4_quantize(merged, group=64)
+    tok = rand(3, f, seed=40)
+    h = qb.int4_linear_fwd(served, tok)
+    exact = tok.double() @ qb.int4_dequantize(served).double().t()
+    within(h, exact, exact.abs() * 2.0 ** -7 + (tok.double().abs() @ merged.double().abs().t()) * 2.0 ** -7)
+    full = tok.double() @ merged.double().t()
+    assert float((h.double() - full).norm() / full.norm()) < 0.25  # 4 bits

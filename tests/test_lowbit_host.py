@@ -94,6 +94,42 @@ def test_swiglu_refusals(lib, qb):
     assert lib.qn_launch_count(0) == before
 
 
+def test_lora_grads_act8_refusals(lib, qb):
+    r = ctypes.byref
+    x = _act8(qb)  # 4 x 128
+    gh, A, B, ga, gb, ws = (P(0x400000 + 0x100000 * i) for i in range(6))
+    f = lib.qlora_lora_grads_act8
+    size = qb.lora_grads_act8_workspace_size(4, 16)
+    assert size == 2 * 16 * 16 * 4
+
+    def call(x=x, gh=gh, n=96, A=A, B=B, rank=16, alpha=32.0, d=None, ga=ga, gb=gb, ws=ws, size=size):
+        return f(None if x is None else r(x), gh, n, A, B, rank, alpha, None if d is None else r(d), ga, gb, ws, size,
+                 None)
+
+    assert call(x=None) == EINVAL
+    assert call(x=_act8(qb, cols=96)) == ESHAPE
+    assert call(x=qb.CAct8(4, 128, None, 0x110000)) == EINVAL
+    assert call(n=-1) == EINVAL
+    assert call(rank=0) == EINVAL and call(rank=257, size=1 << 20) == EINVAL
+    assert call(alpha=float("inf")) == EINVAL and call(alpha=float("nan")) == EINVAL
+    assert call(d=qb.CDropout(1.0, 1, 0)) == EINVAL and call(d=qb.CDropout(float("nan"), 1, 0)) == EINVAL
+    assert call(gh=None) == EINVAL and call(A=None) == EINVAL and call(B=None) == EINVAL
+    assert call(ga=None) == EINVAL and call(gb=None) == EINVAL
+    assert call(gh=P(0x400002)) == EALIGN and call(A=P(0x500008)) == EALIGN and call(gb=P(0x800002)) == EALIGN
+    assert call(ws=None) == 5 and call(size=size - 1) == 5  # QN_EWORKSPACE
+    assert call(ws=P(0x900010)) == EALIGN
+    assert call(ga=gb) == EINVAL  # both gradients in one buffer
+    assert call(ga=A) == EINVAL and call(gb=P(0x400000 + 64)) == EINVAL and call(ws=ga) == EINVAL
+    assert call(ga=P(0x100000)) == EINVAL  # over the codes
+    before = lib.qn_launch_count(0)
+    assert f(r(qb.CAct8(4, 0, None, None)), None, 0, None, None, 16, 1.0, None, None, None, None, 0, None) == OK
+    assert lib.qn_launch_count(0) == before
+    v = ctypes.c_size_t()
+    assert lib.qlora_lora_grads_act8_workspace_size(-1, 16, r(v)) == EINVAL
+    assert lib.qlora_lora_grads_act8_workspace_size(4, 300, r(v)) == EINVAL
+    assert lib.qlora_lora_grads_act8_workspace_size(4, 16, None) == EINVAL
+
+
 def test_int4_sizes(lib, qb):
     assert qb.int4_sizes(32, 256, 64) == (32 * 128, 2 * 32 * 4, 32 * 4)
     assert qb.int4_sizes(5, 64, 32) == (160, 20, 10)
@@ -184,6 +220,19 @@ def test_reference_int4_covers_its_range():
     assert s[1, 0] == 0.0 and z[1, 0] == 0 and q[1].max() == 0
     q, s, z = ref.int4(W[:1], 32, False)
     assert z[0, 0] == 8 and q[0, :2].tolist() == [1, 15]
+
+
+def test_reference_adapter_gradients_against_differences():
+    torch.manual_seed(1)
+    x, gh, A, B = (torch.randn(*s, dtype=torch.float64) for s in ((7, 64), (7, 5), (3, 64), (5, 3)))
+    ga, gb, *_ = ref.lora_grads(x, gh, A, B, 0.5)
+    loss = lambda A, B: float((gh * (0.5 * (x @ A.t()) @ B.t())).sum())  # noqa: E731
+    for g, P_, i in ((ga, A, (1, 9)), (gb, B, (4, 2))):
+        e = torch.zeros_like(P_)
+        e[i] = 1e-6
+        hi = loss(A + e, B) if P_ is A else loss(A, B + e)
+        lo = loss(A - e, B) if P_ is A else loss(A, B - e)
+        assert abs((hi - lo) / 2e-6 - float(g[i])) < 1e-6 * max(1.0, abs(float(g[i])))
 
 
 def test_reference_swiglu_gradient_against_differences():
