@@ -31,4 +31,12 @@ cudaError_t launch_act8_grads(const int8_t *codes, const uint16_t *absmax, const
                               int64_t k, const uint16_t *A, const uint16_t *B, int r, float s, const DropoutArgs &drop,
                               float *grad_A, float *grad_B, void *ws, cudaStream_t st);
 
+// The same on the 5th-generation tensor cores, for what act8_grads_tc_supported: rows of grad_h and of B that
+// TMA can read.
+size_t act8_grads_tc_workspace_bytes(int64_t M, int r);
+bool act8_grads_tc_supported(int64_t M, int64_t n, int r);
+cudaError_t launch_act8_grads_tc(const int8_t *codes, const uint16_t *absmax, const uint16_t *gh, int64_t M, int64_t n,
+                                 int64_t k, const uint16_t *A, const uint16_t *B, int r, float s,
+                                 const DropoutArgs &drop, float *grad_A, float *grad_B, void *ws, cudaStream_t st);
+
 }  // namespace qn

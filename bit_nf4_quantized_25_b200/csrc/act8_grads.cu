@@ -10,10 +10,10 @@
 // in fp32: to the 64-feature partial sums of t, and to u before the second product.
 //
 // Results are fp32 and meant to be as good: t and u are kept in fp32 between the two kernels and enter
-// the second product as two bf16 terms, v = hi + lo, which leaves 2^-17 of v. All sums are fp32 in a fixed
-// order.
+// the second product as three bf16 terms (24 bits). All sums are fp32 in a fixed order.
 //
-// Two kernels, each reading the codes and grad_h once, straight into registers; the second finds in L2
+// These are the kernels for any rank and any width of grad_h, and for short batches; act8_grads_tc.cu has those for long
+// ones. Two kernels, each reading the codes and grad_h once, straight into registers; the second finds in L2
 // what fits there.
 //   k_down   t and u: a warp has 32 tokens, a CTA 128, a cluster splits the features; the adapter's factors go
 //            through shared memory in pieces of 64 features.
@@ -332,13 +332,16 @@ constexpr int kOutThreads = 32 * kColWarps * kTokWarps;
 constexpr int kOutCols = 64 * kColWarps;
 constexpr int kOutRow = kOutCols + 4;  // floats per row j of the sums in shared memory
 
-// v = hi + lo as bf16 pairs: (v0, v1) and (v2, v3).
-__device__ __forceinline__ void split(const float (&v)[4], uint32_t (&hi)[2], uint32_t (&lo)[2]) {
+// v as a sum of three bf16, pairs (v0, v1) and (v2, v3) of each.
+__device__ __forceinline__ void split(float (&v)[4], uint32_t (&part)[3][2]) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        hi[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-        lo[i] = pack_bf16x2(v[2 * i] - bf16_lo(hi[i]), v[2 * i + 1] - bf16_hi(hi[i]));
-    }
+    for (int term = 0; term < 3; ++term)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            part[term][i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+            v[2 * i] -= bf16_lo(part[term][i]);
+            v[2 * i + 1] -= bf16_hi(part[term][i]);
+        }
 }
 
 template <int NT, bool kX, bool kDrop, bool kAligned>
@@ -421,12 +424,13 @@ __device__ __forceinline__ void outer(const GradArgs &p, float *red, int64_t til
 #pragma unroll
                 for (int i = 0; i < 4; ++i) w[i] *= sc[i];
             }
-            uint32_t h[2], l[2];
-            split(w, h, l);
+            uint32_t part[3][2];
+            split(w, part);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mma_16816(acc[i][nt], a[i][0], a[i][1], a[i][2], a[i][3], h[0], h[1]);
+            for (int term = 0; term < 3; ++term)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mma_16816(acc[i][nt], a[i][0], a[i][1], a[i][2], a[i][3], l[0], l[1]);
+                for (int i = 0; i < 4; ++i)
+                    mma_16816(acc[i][nt], a[i][0], a[i][1], a[i][2], a[i][3], part[term][0], part[term][1]);
         }
     }
 
@@ -540,21 +544,27 @@ cudaError_t launch_nt(const GradArgs &p, int sms, cudaStream_t st) {
     return drop ? launch_pass<NT, true, false>(p, sms, st) : launch_pass<NT, false, false>(p, sms, st);
 }
 
+// Batches from this many tokens on go to the tcgen05 kernels.
+constexpr int64_t kTcTokens = 128;
+
 }  // namespace
 
 size_t act8_grads_workspace_bytes(int64_t M, int r) {
     const size_t one = static_cast<size_t>((M + 15) / 16) * 16 * static_cast<size_t>((r + 7) / 8 * 8) * sizeof(float);
-    return 2 * ((one + 255) & ~size_t(255));
+    const size_t here = 2 * ((one + 255) & ~size_t(255)), tc = act8_grads_tc_workspace_bytes(M, r);
+    return here > tc ? here : tc;
 }
 
 cudaError_t launch_act8_grads(const int8_t *codes, const uint16_t *absmax, const uint16_t *gh, int64_t M, int64_t n,
                               int64_t k, const uint16_t *A, const uint16_t *B, int r, float s, const DropoutArgs &drop,
                               float *grad_A, float *grad_B, void *ws, cudaStream_t st) {
+    if (M >= kTcTokens && act8_grads_tc_supported(M, n, r))
+        return launch_act8_grads_tc(codes, absmax, gh, M, n, k, A, B, r, s, drop, grad_A, grad_B, ws, st);
     int sms = 148;
     cudaError_t e = device_sm_count(&sms);
     if (e != cudaSuccess) return e;
     GradArgs p{codes, absmax, gh, M, n, k, A, B, r, 0, s, grad_A, grad_B, static_cast<float *>(ws), nullptr, drop};
-    p.u = reinterpret_cast<float *>(static_cast<char *>(ws) + act8_grads_workspace_bytes(M, r) / 2);
+    p.u = p.t + (M + 15) / 16 * 16 * ((r + 7) / 8 * 8);
     for (p.j0 = 0; p.j0 < r; p.j0 += 64) {
         const int nt = (r - p.j0 + 7) / 8;
         if (nt <= 1)

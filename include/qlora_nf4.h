@@ -373,7 +373,7 @@ qn_status qlora_lora_grads_act8_workspace_size(int64_t M, int r, size_t *ws_byte
  *   grad_A[j, k] = s * sum_m u[m,j] x[m,k],       u = grad_h B     (r x k_in)
  * A, B, grad_h, grad_A, grad_B as there; dropout (NULL: none) as in
  * qlora_lora_grads_dropout, with x the undropped input. The codes and the bf16
- * operands enter exactly, t and u with 16 bits, all sums are fp32 in a fixed order:
+ * operands enter exactly, t and u with 24 bits, all sums are fp32 in a fixed order:
  * results are bit-reproducible. A token whose t or u is not finite makes every
  * gradient that it enters NaN. M, n_out or k_in 0: the gradients are zero.
  * ws: at least qlora_lora_grads_act8_workspace_size() bytes, 256-byte aligned.

@@ -213,10 +213,10 @@ def check_grads(x8, gh, A, B, alpha, keep=None, dropout=None, **kw):
         x, s = x * keep, s / (1.0 - dropout[0])
     wa, wb, sa, sb = ref.lora_grads(x, gh.double(), A.double(), B.double(), s)
     # In units of the sum of the terms' sizes: t (u) is a chain of fp32 additions, 4 of the tensor core and one fma for
-    # 64 features, and 8 over the cluster (2^-23 each); two bf16 terms leave 2^-16; the products over tokens are a chain
-    # of 2 for 16 tokens, at most M / 16, and 10 over the CTA and cluster (2^-23 each); s and a / 127 2^-23 each.
+    # 64 features, and 8 over the cluster (2^-23 each); three bf16 terms leave 2^-24; the products over tokens are a chain
+    # of 3 for 16 tokens and 10 over the CTA and cluster (2^-23 each); s and a / 127 2^-23 each.
     def unit(features):
-        return ((5 * features / 64 + 8) + (2 * M / 16 + 10) + 4) * 2.0 ** -23 + 2.0 ** -16
+        return ((5 * features / 64 + 8) + (3 * (M / 16 + 1) + 10) + 5) * 2.0 ** -23
     within(ga, wa, sa * unit(n) + 1e-30, "grad_A")
     within(gb, wb, sb * unit(k) + 1e-30, "grad_B")
     return ga, gb

