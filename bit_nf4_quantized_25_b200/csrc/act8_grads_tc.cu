@@ -15,8 +15,8 @@
 //
 //   k_down_tc   one CTA: 128 tokens (the MMA's M) of x or of grad_h, N = r; a cluster splits the features and adds
 //               its sums through distributed shared memory.
-//   k_outer_tc  one CTA: 256 columns of x or of grad_h as two accumulators of 128 (M), N = 3 r, K = tokens; both
-//               operands are read with their M or N index contiguous, as they lie. A cluster splits the
+//   k_outer_tc  one CTA: 256 columns of grad_h as two accumulators of 128 (M), or 128 of x, N = 3 r, K = tokens; grad_h
+//               is read with its M index contiguous, as it lies. A cluster splits the
 //               tokens. The second kernel walks the tokens backwards: what the first read last is still in L2.
 //
 // Warp 0 issues the TMA loads, warp 1 the MMAs, the others convert codes and run the epilogue. Every wait is
@@ -72,14 +72,17 @@ __device__ __forceinline__ void cluster_sum(const float *p, uint32_t ranks, floa
         return;
     }
     v[0] = v[1] = v[2] = v[3] = 0.0f;
-    for (uint32_t c = 0; c < ranks; c += 2) {  // 2, 4 or 8 ranks; two loads in flight
+    for (uint32_t c = 0; c < ranks; c += 2) {  // two loads in flight
         float f[8];
 #pragma unroll
-        for (uint32_t h = 0; h < 2; ++h)
-            asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                         : "=f"(f[4 * h]), "=f"(f[4 * h + 1]), "=f"(f[4 * h + 2]), "=f"(f[4 * h + 3])
-                         : "r"(stream::mapa(smem_u32(p), c + h))
-                         : "memory");
+        for (uint32_t h = 0; h < 2; ++h) {
+            f[4 * h] = f[4 * h + 1] = f[4 * h + 2] = f[4 * h + 3] = 0.0f;
+            if (c + h < ranks)
+                asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                             : "=f"(f[4 * h]), "=f"(f[4 * h + 1]), "=f"(f[4 * h + 2]), "=f"(f[4 * h + 3])
+                             : "r"(stream::mapa(smem_u32(p), c + h))
+                             : "memory");
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = (v[i] + f[i]) + f[4 + i];
     }
@@ -97,18 +100,44 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
         : "r"(taddr));
 }
 
+// 16 lanes x 16 columns: thread (g, t) of the warp gives, for i = 0 .. 3, column 4 i + t of lane g (v[2 i]) and of
+// lane g + 8 (v[2 i + 1]).
+__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] * B[smem desc], bf16 inputs.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 __device__ __forceinline__ uint32_t bf2(__nv_bfloat162 v) { return *reinterpret_cast<const uint32_t *>(&v); }
 __device__ __forceinline__ __nv_bfloat162 as_bf2(uint32_t v) { return *reinterpret_cast<const __nv_bfloat162 *>(&v); }
 
-// A block of 64 codes, a 64-byte swizzled row of shared memory, to a 128-byte swizzled row of bf16 at `hi`. kScaled:
-// times a / 128, as hi + lo, lo kLo bytes behind hi; else the codes themselves. `row` is the row's index in its tile (its
-// low three bits swizzle both). A whole block per thread: with half of one, waits and addresses were half of the
-// instructions, and the warps that convert are bound by issuing them.
-template <bool kScaled, uint32_t kLo, bool kDrop>
-__device__ __forceinline__ void convert_block(uint32_t codes, uint32_t row, float a, const DropoutArgs &drop, uint64_t e0,
-                                              uint32_t hi) {
-    const __nv_bfloat162 f = __float2bfloat162_rn(a * 0.0078125f);
-    const uint32_t src = codes + (((row >> 1) & 3u) << 4), dst = hi + ((row & 7u) << 4);
+// Two int8 codes, in the low bytes of the halves of p (the high bytes may hold anything), as a bf16 pair: 128 + the low
+// seven bits, less 128 or (sign bit) 256; exact.
+__device__ __forceinline__ __nv_bfloat162 code_pair(uint32_t p) {
+    return __hsub2(as_bf2((p & 0x007f007fu) | 0x43004300u), as_bf2((p & 0x00800080u) | 0x43004300u));
+}
+
+// Byte mask of four elements' keep bits.
+__device__ __forceinline__ uint32_t keep_bytes(uint32_t b) {
+    return ((b & 1u) | (b & 2u) << 7 | (b & 4u) << 14 | (b & 8u) << 21) * 0xffu;
+}
+
+// A block of 64 codes, a 64-byte swizzled row of shared memory, to a 128-byte swizzled row of bf16. `row` is the row's
+// index in its tile (its low three bits swizzle both). A whole block per thread: with half of one, waits and addresses
+// were half of the instructions, and the warps that convert are bound by issuing them.
+template <bool kDrop>
+__device__ __forceinline__ void convert_block(uint32_t codes, uint32_t row, const DropoutArgs &drop, uint64_t e0, uint32_t to) {
+    const uint32_t src = codes + (((row >> 1) & 3u) << 4), dst = to + ((row & 7u) << 4);
 #pragma unroll
     for (uint32_t c = 0; c < 4; ++c) {
         uint32_t w[4];
@@ -116,33 +145,68 @@ __device__ __forceinline__ void convert_block(uint32_t codes, uint32_t row, floa
         if (kDrop) {
             const uint32_t keep = dropout_keep_bits(drop, e0 + 16 * c, 16);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t b = keep >> (4 * i);
-                w[i] &= ((b & 1u) | (b & 2u) << 7 | (b & 4u) << 14 | (b & 8u) << 21) * 0xffu;
-            }
+            for (int i = 0; i < 4; ++i) w[i] &= keep_bytes(keep >> (4 * i));
         }
 #pragma unroll
         for (uint32_t h = 0; h < 2; ++h) {
-            uint32_t oh[4], ol[4];
+            uint32_t o[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                // two codes as a bf16 pair: 128 + the low seven bits, less 128 or (sign bit) 256; exact
-                const uint32_t p = __byte_perm(w[2 * h + (i >> 1)], 0u, (i & 1) ? 0x4342 : 0x4140);
-                const __nv_bfloat162 q =
-                    __hsub2(as_bf2((p & 0x007f007fu) | 0x43004300u), as_bf2((p & 0x00800080u) | 0x43004300u));
-                if (kScaled) {
-                    const __nv_bfloat162 top = __hmul2(q, f);
-                    oh[i] = bf2(top);
-                    ol[i] = bf2(__hfma2(q, f, __hneg2(top)));
-                } else {
-                    oh[i] = bf2(q);
-                }
-            }
-            const uint32_t to = dst ^ ((2 * c + h) << 4);
-            sts128(to, oh);
-            if (kScaled) sts128(to + kLo, ol);
+            for (int i = 0; i < 4; ++i) o[i] = bf2(code_pair(__byte_perm(w[2 * h + (i >> 1)], 0u, (i & 1) ? 0x4342 : 0x4140)));
+            sts128(dst ^ ((2 * c + h) << 4), o);
         }
     }
+}
+
+// Barriers by their shared-window address (slot s of a ring at bar + 8 s): what the one thread that issues the MMAs
+// spends on addresses shows in every step.
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes) : "memory");
+}
+// Bounded, as sm100::mbar_wait.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+    for (uint32_t i = 0; i < (1u << 24); ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok) return true;
+    }
+    return false;
+}
+// Whether the phase is over; does not wait.
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// An arrival when every MMA that this thread has issued is done.
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tma(uint32_t dst, const CUtensorMap *m, uint32_t bar, int32_t c0, int32_t c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
 }
 
 // A place in a ring of n slots: the slot, and the parity of its phase in this round. (Slot and phase by division of a
@@ -159,32 +223,14 @@ struct Ring {
 };
 
 // Waits for the last phase that `count` steps put on each of n barriers; `at` is the place behind the last step.
-__device__ __forceinline__ void wait_out(uint64_t *bars, int n, int count, Ring at) {
+__device__ __forceinline__ void wait_out(uint32_t bars, int n, int count, Ring at) {
     for (int e = count < n ? count : n; e > 0; --e) {
         if (--at.slot < 0) {
             at.slot = n - 1;
             at.phase ^= 1u;
         }
-        mbar_wait(&bars[at.slot], at.phase);
+        bar_wait(bars + 8 * at.slot, at.phase);
     }
-}
-
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect() {
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
-    return ok != 0;
-}
-
-// Whether the phase is over; does not wait.
-__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
 }
 
 // The producer of the codes and of the second operand (the factor, or t or u): two rings that empty at their own
@@ -192,18 +238,18 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
 // go out only when the codes' slot is free, and its latency would be in every step. Issues what has room until all
 // `steps` are out; gives up after about a second without progress. Returns false then.
 template <typename Codes, typename Second>
-__device__ __forceinline__ bool feed(int steps, int &ci, Ring &c, int slots, uint64_t *cempty, Codes &&codes, int &ri, Ring &r,
-                                     int rslots, uint64_t *rempty, Second &&second, volatile uint32_t *abort_flag) {
+__device__ __forceinline__ bool feed(int steps, int &ci, Ring &c, int slots, uint32_t cempty, Codes &&codes, int &ri, Ring &r,
+                                     int rslots, uint32_t rempty, Second &&second, volatile uint32_t *abort_flag) {
     uint32_t idle = 0;
     while (ci < steps || ri < steps) {
         bool did = false;
-        if (ri < steps && (ri < rslots || mbar_test(&rempty[r.slot], r.phase ^ 1u))) {
+        if (ri < steps && (ri < rslots || bar_test(rempty + 8 * r.slot, r.phase ^ 1u))) {
             second(ri, r.slot);
             ++ri;
             r.next(rslots);
             did = true;
         }
-        if (ci < steps && (ci < slots || mbar_test(&cempty[c.slot], c.phase ^ 1u))) {
+        if (ci < steps && (ci < slots || bar_test(cempty + 8 * c.slot, c.phase ^ 1u))) {
             codes(ci, c.slot);
             ++ci;
             c.next(slots);
@@ -216,20 +262,23 @@ __device__ __forceinline__ bool feed(int steps, int &ci, Ring &c, int slots, uin
 }
 
 // A warp that brings the absmaxes of coming steps to shared memory, four steps (a batch) at a time in a ring of
-// three batches of kGroups x 4 values: `at(step, group)` points at four neighbouring ones, of which `count` exist. In the
-// converting warps themselves the loads' latency showed in every fourth step.
+// three batches of kGroups x kN values: `at(step, group, count)` points at kN neighbouring ones, of which `count` exist,
+// and `put(batch, group, values)` stores them. In the converting warps themselves the loads' latency showed in every fourth step.
 constexpr int kBatch = 4, kBatches = 3;
 
-__device__ __forceinline__ uint64_t load4(const uint16_t *p, int count) {
-    if (count >= 4 && (reinterpret_cast<uintptr_t>(p) & 7u) == 0) return __ldg(reinterpret_cast<const unsigned long long *>(p));
+// kN (2 or 4) neighbouring ones at p, of which `count` exist.
+template <int kN>
+__device__ __forceinline__ uint64_t load_few(const uint16_t *p, int count) {
+    if (count >= kN && (reinterpret_cast<uintptr_t>(p) & (2u * kN - 1u)) == 0)
+        return kN == 4 ? __ldg(reinterpret_cast<const unsigned long long *>(p)) : ld_ro_u32(p);
     uint64_t v = 0;
 #pragma unroll 1
-    for (int i = 0; i < count && i < 4; ++i) v |= static_cast<uint64_t>(ld_ro_u16(p + i)) << (16 * i);
+    for (int i = 0; i < count && i < kN; ++i) v |= static_cast<uint64_t>(ld_ro_u16(p + i)) << (16 * i);
     return v;
 }
 
-template <int kGroups, typename At>
-__device__ __forceinline__ bool load_absmax(int steps, uint64_t *ring, uint64_t *afull, uint64_t *aempty, int lane, At &&at) {
+template <int kN, int kGroups, typename At, typename Put>
+__device__ __forceinline__ bool load_absmax(int steps, uint32_t afull, uint32_t aempty, int lane, At &&at, Put &&put) {
     Ring b;
     for (int i = 0; i < steps; i += kBatch, b.next(kBatches)) {
         uint64_t v[kGroups / 32];
@@ -237,13 +286,13 @@ __device__ __forceinline__ bool load_absmax(int steps, uint64_t *ring, uint64_t 
         for (int g = 0; g < kGroups / 32; ++g) {
             int count;
             const uint16_t *p = at(i, 32 * g + lane, count);
-            v[g] = load4(p, count);
+            v[g] = load_few<kN>(p, count);
         }
-        if (i >= kBatches * kBatch && !mbar_wait(&aempty[b.slot], b.phase ^ 1u)) return false;
+        if (i >= kBatches * kBatch && !bar_wait(aempty + 8 * b.slot, b.phase ^ 1u)) return false;
 #pragma unroll
-        for (int g = 0; g < kGroups / 32; ++g) ring[b.slot * kGroups + 32 * g + lane] = v[g];
+        for (int g = 0; g < kGroups / 32; ++g) put(b.slot, 32 * g + lane, v[g]);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&afull[b.slot]);
+        if (lane == 0) bar_arrive(afull + 8 * b.slot);
     }
     return true;
 }
@@ -274,9 +323,9 @@ template <bool kX, bool kDrop>
 __device__ __forceinline__ void down_tc(const CUtensorMap *act, const CUtensorMap *factor, const TcArgs &p, uint8_t *smem,
                                         uint64_t *bars, int64_t tile, uint32_t rank, uint32_t ranks) {
     constexpr int kStages = kX ? kDownStagesX : kDownStagesGh;
-    uint64_t *full = bars, *empty = full + 4, *cfull = empty + 4, *cempty = cfull + 4;
-    uint64_t *afull = cempty + 4, *aempty = afull + kBatches, *done = aempty + kBatches;
-    uint32_t *slot = reinterpret_cast<uint32_t *>(done + 1);
+    const uint32_t base = smem_u32(smem), full = smem_u32(bars), empty = full + 32, cfull = empty + 32, cempty = cfull + 32;
+    const uint32_t afull = cempty + 32, aempty = afull + 8 * kBatches, done = aempty + 8 * kBatches;
+    uint32_t *slot = reinterpret_cast<uint32_t *>(bars + 16 + 2 * kBatches + 1);
     volatile uint32_t *abort_flag = slot + 1;
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const int64_t pieces = ((kX ? p.k : p.n) + kK - 1) / kK;
@@ -286,21 +335,21 @@ __device__ __forceinline__ void down_tc(const CUtensorMap *act, const CUtensorMa
     // a stage: the tile and the factor's piece; kX: the codes behind the stages
     const uint32_t piece = kX ? static_cast<uint32_t>(p.rp) * 128u : kChunk, stage = kDownA + piece;
     const int slots = down_codes(p.rp);
-    uint8_t *codes = smem + kStages * stage;
+    const uint32_t codes = base + kStages * stage;
     uint16_t *absmax = reinterpret_cast<uint16_t *>(smem + kDownRing);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < 4; ++s) {
-            mbar_init(&full[s], kX ? 1 + kDownWarps / 2 : 1);  // TMA: the factor's piece and grad_h's tile; kX: the converted tile
-            mbar_init(&empty[s], 1);                           // the stage's MMAs are done
-            mbar_init(&cfull[s], 1);                           // TMA: codes
-            mbar_init(&cempty[s], kDownWarps / 2);             // the group's warps have read them
+            bar_init(full + 8 * s, kX ? 1 + kDownWarps / 2 : 1);  // TMA: the factor's piece and grad_h's tile; kX: the converted tile
+            bar_init(empty + 8 * s, 1);                           // the stage's MMAs are done
+            bar_init(cfull + 8 * s, 1);                // kX: TMA, codes; else an accumulator's segment is done
+            bar_init(cempty + 8 * s, kDownWarps / 2);  // the group's warps have read the codes, or the accumulator
         }
         for (int s = 0; s < kBatches; ++s) {
-            mbar_init(&afull[s], 1);
-            mbar_init(&aempty[s], kDownWarps);
+            bar_init(afull + 8 * s, 1);
+            bar_init(aempty + 8 * s, kDownWarps);
         }
-        mbar_init(done, 1);
+        bar_init(done, 1);
         *abort_flag = 0u;
         fence_barrier_init();
     }
@@ -318,12 +367,11 @@ __device__ __forceinline__ void down_tc(const CUtensorMap *act, const CUtensorMa
     const uint32_t tmem = *slot;
     grid_dependents_launch();
     // The tensor core cuts off what it adds instead of rounding it, so a long chain of MMAs drifts (448 of them: 1.6e-5
-    // of the sum). grad_h: the K steps go round `accs` accumulators, which the epilogue adds. x: the codes go in as they
-    // are, 64 features to a fresh accumulator, and the converting warps add it up times a / 128 in fp32.
-    const int accs = p.rp <= 32 ? 8 : 4;
+    // of the sum). So there are four accumulators, taken in turn and added up in fp32 registers by the other warps: of x,
+    // whose codes go in as they are, one for each 64 features, times a / 128; of grad_h, one for each kSegment stages.
+    constexpr int kSegment = 8;
 
-    // Warps 2 .. 9 have 32 lanes (tokens) of the accumulators each: of x all columns of every other step, of grad_h every
-    // other accumulator.
+    // Warps 2 .. 9 have 32 lanes (tokens) of the accumulators each, of every other one.
     const uint32_t quarter = static_cast<uint32_t>(warp & 3);
     const int group = (warp - 2) >> 2;
     float sum[4][16];
@@ -352,14 +400,14 @@ __device__ __forceinline__ void down_tc(const CUtensorMap *act, const CUtensorMa
                 if (!feed(
                         steps, ci, c, slots, cempty,
                         [&](int i, int q) {
-                            mbar_arrive_expect_tx(&cfull[q], kDownA / 2);
+                            bar_expect(cfull + 8 * q, kDownA / 2);
                             for (int h = 0; h < 2; ++h)
-                                tma_load_2d(codes + q * (kDownA / 2) + h * 4096, act, &cfull[q], static_cast<int32_t>((lo + i) * kK), tok0 + 64 * h);
+                                tma(codes + q * (kDownA / 2) + h * 4096, act, cfull + 8 * q, static_cast<int32_t>((lo + i) * kK), tok0 + 64 * h);
                         },
                         ri, r, kStages, empty,
                         [&](int i, int q) {
-                            mbar_arrive_expect_tx(&full[q], piece);
-                            tma_load_2d(smem + q * stage + kDownA, factor, &full[q], static_cast<int32_t>((lo + i) * kK), p.j0);
+                            bar_expect(full + 8 * q, piece);
+                            tma(base + q * stage + kDownA, factor, full + 8 * q, static_cast<int32_t>((lo + i) * kK), p.j0);
                         },
                         abort_flag))
                     *abort_flag = 1u;
@@ -370,16 +418,16 @@ __device__ __forceinline__ void down_tc(const CUtensorMap *act, const CUtensorMa
                 int i = 0;
                 Ring r;
                 for (; i < steps && !*abort_flag; ++i, r.next(kStages)) {
-                    if (i >= kStages && !mbar_wait(&empty[r.slot], r.phase ^ 1u)) {
+                    if (i >= kStages && !bar_wait(empty + 8 * r.slot, r.phase ^ 1u)) {
                         *abort_flag = 1u;
                         break;
                     }
-                    uint8_t *st = smem + r.slot * stage;
+                    const uint32_t st = base + r.slot * stage;
                     const int32_t c0 = static_cast<int32_t>((lo + i) * kK);
-                    mbar_arrive_expect_tx(&full[r.slot], stage);
-                    tma_load_2d(st, act, &full[r.slot], c0, tok0);
-                    tma_load_2d(st + kChunk, act, &full[r.slot], c0, tok0 + 64);
-                    tma_load_2d(st + kDownA, factor, &full[r.slot], p.j0, c0);  // 64 rows of B
+                    bar_expect(full + 8 * r.slot, stage);
+                    tma(st, act, full + 8 * r.slot, c0, tok0);
+                    tma(st + kChunk, act, full + 8 * r.slot, c0, tok0 + 64);
+                    tma(st + kDownA, factor, full + 8 * r.slot, p.j0, c0);  // 64 rows of B
                 }
                 wait_out(full, kStages, i, r);
             }
@@ -390,36 +438,44 @@ __device__ __forceinline__ void down_tc(const CUtensorMap *act, const CUtensorMa
         const bool leader = elect();
         const uint32_t idesc = idesc_bf16(kDownTile, p.rp, 0, kX ? 0 : 1);
         // the descriptors of slot 0; a slot or a K step further is an addition to the address (in 16-byte units)
-        const uint64_t a0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
-        const uint64_t b0 = kX ? smem_desc_sw128(smem_u32(smem) + kDownA, 16, 1024) : smem_desc_sw128(smem_u32(smem) + kDownA, kChunk, 1024);
+        const uint64_t a0 = smem_desc_sw128(base, 16, 1024);
+        const uint64_t b0 = kX ? smem_desc_sw128(base + kDownA, 16, 1024) : smem_desc_sw128(base + kDownA, kChunk, 1024);
         int i = 0;
-        Ring r;
+        Ring r, q;  // stages; grad_h: accumulators
         for (; i < steps; ++i, r.next(kStages)) {
-            if (!mbar_wait(&full[r.slot], r.phase)) break;
+            if (!bar_wait(full + 8 * r.slot, r.phase)) break;
+            if (!kX && i % kSegment == 0 && i >= 4 * kSegment && !bar_wait(cempty + 8 * q.slot, q.phase ^ 1u)) break;
             __syncwarp();
             tc_fence_after();
             const uint64_t a = a0 + r.slot * (stage / 16), b = b0 + r.slot * (stage / 16);
-            const uint32_t d = tmem + (kX ? static_cast<uint32_t>(r.slot) : static_cast<uint32_t>(4 * i) & static_cast<uint32_t>(accs - 1)) * p.rp;
-            const uint32_t more = 4 * i >= accs ? 1u : 0u;  // the K steps of a stage start new accumulators together
+            const uint32_t d = tmem + static_cast<uint32_t>(kX ? r.slot : q.slot) * p.rp;
+            const uint32_t more = kX || i % kSegment == 0 ? 0u : 1u;
+            const bool last = !kX && (i % kSegment == kSegment - 1 || i + 1 == steps);
             if (leader) {
 #pragma unroll
-                for (uint32_t kk = 0; kk < 4; ++kk)
-                    mma_bf16_ss(kX ? d : d + kk * p.rp, a + 2 * kk, b + (kX ? 2 : 128) * kk, idesc, kX ? (kk > 0 ? 1u : 0u) : more);
-                mma_commit(&empty[r.slot]);
+                for (uint32_t kk = 0; kk < 4; ++kk) mma_bf16_ss(d, a + 2 * kk, b + (kX ? 2 : 128) * kk, idesc, kk > 0 ? 1u : more);
+                commit(empty + 8 * r.slot);
+                if (last) commit(cfull + 8 * q.slot);
             }
             __syncwarp();
+            if (last) q.next(4);
         }
         if (i < steps) *abort_flag = 1u;
-        if (leader) mma_commit(done);
-        wait_out(empty, kStages, i, r);  // every commit has arrived before the CTA may leave
+        if (leader) commit(done);
+        // every commit has arrived before the CTA may leave
+        wait_out(empty, kStages, i, r);
+        if (!kX && i == steps) wait_out(cfull, 4, (steps + kSegment - 1) / kSegment, q);
     } else if (kX && warp == kDownThreads / 32 - 1) {
         const int64_t blocks = p.k / kBlock;
         // a group: the batch's four steps of a token
-        if (!load_absmax<kDownTile>(steps, reinterpret_cast<uint64_t *>(absmax), afull, aempty, lane, [&](int i, int row, int &count) {
-                const int64_t m = tok0 + static_cast<int64_t>(row);
-                count = m < p.M ? steps - i : 0;
-                return p.absmax + (m < p.M ? m : 0) * blocks + lo + i;
-            }))
+        if (!load_absmax<4, kDownTile>(
+                steps, afull, aempty, lane,
+                [&](int i, int row, int &count) {
+                    const int64_t m = tok0 + static_cast<int64_t>(row);
+                    count = m < p.M ? steps - i : 0;
+                    return p.absmax + (m < p.M ? m : 0) * blocks + lo + i;
+                },
+                [&](int batch, int row, uint64_t v) { reinterpret_cast<uint64_t *>(absmax)[batch * kDownTile + row] = v; }))
             *abort_flag = 1u;
     } else if (kX) {
         const uint32_t row = (threadIdx.x - 64) & 127u;  // a token
@@ -435,7 +491,7 @@ __device__ __forceinline__ void down_tc(const CUtensorMap *act, const CUtensorMa
         for (int i = group; ok && i < steps + kStages; i += 2) {
             const int e = i - kStages, q = e & (kBatch - 1);
             if (e >= 0) {
-                ok = (q > 1 || mbar_wait(&afull[b.slot], b.phase)) && mbar_wait(&empty[r.slot], r.phase ^ 1u);
+                ok = (q > 1 || bar_wait(afull + 8 * b.slot, b.phase)) && bar_wait(empty + 8 * r.slot, r.phase ^ 1u);
                 if (!ok) break;
                 tc_fence_after();
                 add(static_cast<uint32_t>(r.slot * p.rp),
@@ -443,21 +499,21 @@ __device__ __forceinline__ void down_tc(const CUtensorMap *act, const CUtensorMa
                 tc_fence_before();
                 __syncwarp();
                 if (q > 1) {
-                    if (lane == 0) mbar_arrive(&aempty[b.slot]);
+                    if (lane == 0) bar_arrive(aempty + 8 * b.slot);
                     b.next(kBatches);
                 }
             }
             if (i < steps) {
-                ok = mbar_wait(&cfull[c.slot], c.phase);
+                ok = bar_wait(cfull + 8 * c.slot, c.phase);
                 if (!ok) break;
-                convert_block<false, 0u, kDrop>(smem_u32(codes) + c.slot * (kDownA / 2) + row * 64u, row, 1.0f, p.drop,
-                                                p.drop.offset + static_cast<uint64_t>(m * p.k + (lo + i) * kK),
-                                                smem_u32(smem) + r.slot * stage + row * 128u);
+                convert_block<kDrop>(codes + c.slot * (kDownA / 2) + row * 64u, row, p.drop,
+                                     p.drop.offset + static_cast<uint64_t>(m * p.k + (lo + i) * kK),
+                                     base + r.slot * stage + row * 128u);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&cempty[c.slot]);
-                    mbar_arrive(&full[r.slot]);
+                    bar_arrive(cempty + 8 * c.slot);
+                    bar_arrive(full + 8 * r.slot);
                 }
             }
             r.next(kStages);
@@ -466,16 +522,30 @@ __device__ __forceinline__ void down_tc(const CUtensorMap *act, const CUtensorMa
             c.next(slots);
         }
         if (!ok) *abort_flag = 1u;
+    } else if (warp < 2 + kDownWarps) {
+        Ring q;
+        if (group == 1) q.next(4);
+        for (int i = group * kSegment; i < steps; i += 2 * kSegment) {
+            if (!bar_wait(cfull + 8 * q.slot, q.phase)) {
+                *abort_flag = 1u;
+                break;
+            }
+            tc_fence_after();
+            add(static_cast<uint32_t>(q.slot * p.rp), 1.0f);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(cempty + 8 * q.slot);
+            q.next(4);
+            q.next(4);
+        }
     }
     __syncthreads();  // every load has landed: the ring is free for the sums
 
     // the CTA's sums to shared memory, a row per token; the second group's next to the first's
     float *red = reinterpret_cast<float *>(smem);
     if (warp >= 2 && warp < 2 + kDownWarps) {
-        const bool ok = mbar_wait(done, 0) && !*abort_flag;
+        const bool ok = bar_wait(done, 0) && !*abort_flag;
         tc_fence_after();
-        if (!kX)
-            for (int q = group; q < accs && q < 4 * steps; q += 2) add(static_cast<uint32_t>(q * p.rp), 1.0f);
         float4 *dst = reinterpret_cast<float4 *>(red + (group * kDownTile + quarter * 32 + lane) * kDownRedRow);
         const float nan = __uint_as_float(0x7fc00000u);
 #pragma unroll
@@ -548,67 +618,63 @@ k_down_tc(const __grid_constant__ CUtensorMap tm_gh, const __grid_constant__ CUt
 
 // ------------------------------------------------------------------------ products over tokens
 
-constexpr int kOutCols = 256;
-constexpr int kOutWarps = 16;  // converters, four groups with a slot each that take steps in turn
-constexpr int kTokX = 32;      // tokens per step of x: with 64 and two slots a slot's round trip was the bound
+constexpr int kColsGh = 256, kColsX = 128;
+constexpr int kOutWarps = 16;  // converters: four groups that take steps in turn, each with its slot of TMEM
 constexpr int kOutThreads = 96 + 32 * kOutWarps;  // with the producer, the MMA and the absmax warp
-constexpr int kDrain = 16;  // steps (4 MMAs on an accumulator each) between two drains
-constexpr uint32_t kOutA = 4 * kChunk;  // 64 tokens x 256 columns
-constexpr int kOutRowX = kOutCols + 4;  // floats per row j of the sums of x
-constexpr int kOutRowGh = 68;           // floats per column of grad_h of its sums
-constexpr uint32_t kOutAbsmax = kBatches * kBatch * kTokX * 8;
-constexpr uint32_t kOutRed = kOutCols * kOutRowGh * 4;
-static_assert(64 * kOutRowX * 4 <= kOutRed, "");
-constexpr int kOutStagesX = 4;
-constexpr uint32_t kOutTileX = kTokX * kOutCols * 2;  // bytes of hi, or of lo
-constexpr uint32_t kChunkX = kTokX * 64 * 2;
+constexpr uint32_t kTmemA = 256;  // x: columns of A, 32 hi and 32 lo for each group; the accumulator has at most 192
+constexpr uint32_t kOutA = 4 * kChunk;      // 64 tokens x 256 columns of grad_h
+constexpr uint32_t kOutCodes = kK * kColsX;  // bytes of codes of a step
+constexpr int kMaxStages = 8;
+constexpr uint32_t kOutRoom = 200 * 1024;
 
-// For a row of t or u of 1, 2 or 3 pieces: stages of grad_h, each with t; of x four, with u and codes.
-__host__ __device__ constexpr int out_stages(int chunks) { return chunks == 1 ? 5 : chunks == 2 ? 4 : 3; }
-__host__ __device__ constexpr uint32_t out_ring(int chunks) {
-    const uint32_t gh = static_cast<uint32_t>(out_stages(chunks)) * (kOutA + static_cast<uint32_t>(chunks) * kChunk);
-    const uint32_t x = kOutStagesX * (2 * kOutTileX + static_cast<uint32_t>(chunks) * kChunkX) + kOutStagesX * (kOutTileX / 2);
-    return gh > x ? gh : x;
+// Stages that fit for a row of t or u of `chunks` pieces: grad_h or codes, and t or u.
+__host__ __device__ constexpr int out_stages(bool x, int chunks) {
+    const int fit = static_cast<int>(kOutRoom / ((x ? kOutCodes : kOutA) + static_cast<uint32_t>(chunks) * kChunk));
+    return fit > kMaxStages ? kMaxStages : fit;
 }
-static_assert(out_ring(1) <= 216 * 1024 && out_ring(2) <= 216 * 1024 && out_ring(3) <= 216 * 1024, "");
-static_assert(out_ring(1) >= kOutRed && out_ring(2) >= kOutRed && out_ring(3) >= kOutRed, "");
+constexpr uint32_t kOutAbsmax = kBatches * kBatch * 2 * kK * 2;
+constexpr int kOutRowX = kColsX + 4;  // floats per row j of the sums of x
+constexpr int kOutRowGh = 68;         // floats per column of grad_h of its sums
+static_assert(64 * kOutRowX * 4 <= kOutRoom && kColsGh * kOutRowGh * 4 <= kOutRoom, "");
+constexpr size_t kOutSmem = 1024 + kOutRoom + kOutAbsmax + 512;
 
 template <bool kX, bool kDrop>
 __device__ __forceinline__ void outer_tc(const CUtensorMap *act, const CUtensorMap *mid, const TcArgs &p, uint8_t *smem,
                                          uint64_t *bars, int64_t tile, uint32_t rank, uint32_t ranks) {
-    constexpr int kTok = kX ? kTokX : kK;
-    const int stages = kX ? kOutStagesX : out_stages(p.chunks);
-    constexpr int slots = kOutStagesX;  // of codes
-    const uint32_t mid_bytes = p.chunks * (kX ? kChunkX : kChunk), stage = (kX ? 2 * kOutTileX : kOutA) + mid_bytes;
-    uint64_t *full = bars, *empty = full + 5, *cfull = empty + 5, *cempty = cfull + 5;
-    uint64_t *afull = cempty + 5, *aempty = afull + kBatches, *done = aempty + kBatches, *drained = done + 1;
-    uint32_t *slot = reinterpret_cast<uint32_t *>(drained + 1);
+    constexpr int kCols = kX ? kColsX : kColsGh;
+    constexpr uint32_t kAct = kX ? kOutCodes : kOutA;
+    // Steps between two drains of the accumulators into registers: the tensor core cuts off what it adds instead of
+    // rounding it, and a chain of 256 MMAs would be off by 1e-5.
+    constexpr int kDrain = kX ? 8 : 16;
+    const int stages = out_stages(kX, p.chunks);
+    const uint32_t stage = kAct + p.chunks * kChunk;  // codes or grad_h, then u or t
+    const uint32_t base = smem_u32(smem), full = smem_u32(bars), empty = full + 8 * kMaxStages, ready = empty + 8 * kMaxStages, ufull = ready + 32;
+    const uint32_t afull = ufull + 8 * kMaxStages, aempty = afull + 8 * kBatches, done = aempty + 8 * kBatches, drained = done + 8;
+    uint32_t *slot = reinterpret_cast<uint32_t *>(bars + 3 * kMaxStages + 4 + 2 * kBatches + 2);
     volatile uint32_t *abort_flag = slot + 1;
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const int64_t width = kX ? p.k : p.n;
-    const int32_t col0 = static_cast<int32_t>(tile * kOutCols);
-    const int64_t all = (p.M + kTok - 1) / kTok;
+    const int32_t col0 = static_cast<int32_t>(tile * kCols);
+    const int64_t all = (p.M + kK - 1) / kK;
     const int64_t lo = all * rank / ranks;
     const int steps = static_cast<int>(all * (rank + 1) / ranks - lo);
-    // a stage: the tile (kX: hi and lo), then t or u; kX: the codes behind the stages
-    uint8_t *codes = smem + stages * stage;
-    uint16_t *absmax = reinterpret_cast<uint16_t *>(smem + out_ring(p.chunks));
+    uint16_t *absmax = reinterpret_cast<uint16_t *>(smem + kOutRoom);
     // step i works on the tokens from tok(i) on: the last ones first
-    auto tok = [&](int i) { return static_cast<int32_t>((lo + steps - 1 - i) * kTok); };
+    auto tok = [&](int i) { return static_cast<int32_t>((lo + steps - 1 - i) * kK); };
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < 5; ++s) {
-            mbar_init(&full[s], kX ? 1 + kOutWarps / 4 : 1);  // TMA: t or u, and grad_h; kX: the group's tile
-            mbar_init(&empty[s], 1);
-            mbar_init(&cfull[s], 1);
-            mbar_init(&cempty[s], kOutWarps / 4);
+        for (int s = 0; s < kMaxStages; ++s) {
+            bar_init(full + 8 * s, 1);   // TMA: grad_h and t; kX: the codes
+            bar_init(ufull + 8 * s, 1);  // kX: TMA, u
+            bar_init(empty + 8 * s, 1);  // the stage's MMAs are done
         }
+        for (int s = 0; s < 4; ++s) bar_init(ready + 8 * s, 4);  // kX: the group has put a step's A into TMEM
         for (int s = 0; s < kBatches; ++s) {
-            mbar_init(&afull[s], 1);
-            mbar_init(&aempty[s], kOutWarps);
+            bar_init(afull + 8 * s, 1);
+            bar_init(aempty + 8 * s, kOutWarps);
         }
-        mbar_init(done, 1);             // the MMAs up to a drain are done
-        mbar_init(drained, kOutWarps);  // the warps have read the accumulators
+        bar_init(done, 1);             // the MMAs up to a drain are done
+        bar_init(drained, kOutWarps);  // the warps have read the accumulators
         *abort_flag = 0u;
         fence_barrier_init();
     }
@@ -625,22 +691,24 @@ __device__ __forceinline__ void outer_tc(const CUtensorMap *act, const CUtensorM
     tc_fence_after();
     const uint32_t tmem = *slot;
 
-    // The accumulators are emptied into registers every kDrain steps: the tensor core cuts off what it adds instead of
-    // rounding it, and a chain of 256 MMAs would be off by 1e-5. Warps 2 .. 17 have 32 lanes (columns) of one of the two
-    // accumulators each, and every other 16 of the columns j.
-    const uint32_t quarter = static_cast<uint32_t>(warp & 3), h = (static_cast<uint32_t>(warp - 2) >> 2) & 1u;
-    const int jb0 = (warp - 2) >> 3;
-    float sum[2][16];
+    // Warps 2 .. 17 drain 32 lanes (columns) of an accumulator each: of grad_h's two, every other 16 of the columns j; of
+    // x's, 16 columns j.
+    const uint32_t quarter = static_cast<uint32_t>(warp & 3);
+    const int group = (warp - 2) >> 2;
+    const uint32_t h = kX ? 0u : static_cast<uint32_t>(group & 1);
+    const int jb0 = kX ? group : group >> 1;
+    constexpr int kJs = kX ? 1 : 2;
+    float sum[kJs][16];
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int b = 0; b < kJs; ++b)
 #pragma unroll
         for (int c = 0; c < 16; ++c) sum[b][c] = 0.0f;
     auto drain = [&](uint32_t nth) -> bool {
-        if (!mbar_wait(done, nth & 1u)) return false;
+        if (!bar_wait(done, nth & 1u)) return false;
         tc_fence_after();
         const uint32_t d = tmem + 256 * h + ((quarter * 32u) << 16);
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < kJs; ++b) {
             const int j = 16 * (jb0 + 2 * b);
             if (j < p.rp) {
                 uint32_t v0[16], v1[16], v2[16];
@@ -655,115 +723,115 @@ __device__ __forceinline__ void outer_tc(const CUtensorMap *act, const CUtensorM
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(drained);
+        if (lane == 0) bar_arrive(drained);
         return true;
     };
 
     if (warp == 0) {
         if (lane == 0) {
             // Up to the dependency wait only x and grad_h are read, which the preceding kernel reads too.
-            if (kX) {
-                int ci = 0, ri = 0;
-                Ring c, r;
-                auto load_codes = [&](int i, int q) {
-                    mbar_arrive_expect_tx(&cfull[q], kOutTileX / 2);
-                    for (int b = 0; b < 4; ++b)
-                        tma_load_2d(codes + q * (kOutTileX / 2) + b * (kChunkX / 2), act, &cfull[q], col0 + 64 * b, tok(i));
-                };
-                for (; ci < slots && ci < steps; ++ci, c.next(slots)) load_codes(ci, c.slot);
-                grid_dependency_wait();
-                if (!feed(
-                        steps, ci, c, slots, cempty, load_codes, ri, r, stages, empty,
-                        [&](int i, int q) {
-                            mbar_arrive_expect_tx(&full[q], mid_bytes);
-                            for (int e = 0; e < p.chunks; ++e) tma_load_2d(smem + q * stage + 2 * kOutTileX + e * kChunkX, mid, &full[q], 64 * e, tok(i));
-                        },
-                        abort_flag))
-                    *abort_flag = 1u;
-                wait_out(full, stages, ri, r);
-                wait_out(cfull, slots, ci, c);
-            } else {
-                int i = 0, issued = 0;  // steps whose t, and whose grad_h, is on its way
-                Ring ti, gi;
-                auto load_gh = [&]() {
-                    mbar_arrive_expect_tx(&full[gi.slot], stage);
-                    for (int b = 0; b < 4; ++b)
-                        tma_load_2d(smem + gi.slot * stage + b * kChunk, act, &full[gi.slot], col0 + 64 * b, tok(issued));
-                    ++issued;
-                    gi.next(stages);
-                };
-                auto load_t = [&]() {
-                    for (int e = 0; e < p.chunks; ++e)
-                        tma_load_2d(smem + ti.slot * stage + kOutA + e * kChunk, mid, &full[ti.slot], 64 * e, tok(i));
-                    ++i;
-                    ti.next(stages);
-                };
-                while (issued < stages && issued < steps) load_gh();
-                grid_dependency_wait();
-                while (i < steps && !*abort_flag) {
-                    if (i >= issued) {
-                        if (!mbar_wait(&empty[gi.slot], gi.phase ^ 1u)) {
-                            *abort_flag = 1u;
-                            break;
-                        }
-                        load_gh();
+            int i = 0, issued = 0;  // steps whose t or u, and whose activation, is on its way
+            Ring mi, ai;
+            auto load_act = [&]() {
+                bar_expect(full + 8 * ai.slot, kX ? kAct : stage);
+                for (int b = 0; b < kCols / 64; ++b)
+                    tma(base + ai.slot * stage + b * (kAct / (kCols / 64)), act, full + 8 * ai.slot, col0 + 64 * b, tok(issued));
+                ++issued;
+                ai.next(stages);
+            };
+            auto load_mid = [&]() {
+                const uint32_t bar = (kX ? ufull : full) + 8 * mi.slot;
+                if (kX) bar_expect(bar, stage - kAct);
+                for (int e = 0; e < p.chunks; ++e) tma(base + mi.slot * stage + kAct + e * kChunk, mid, bar, 64 * e, tok(i));
+                ++i;
+                mi.next(stages);
+            };
+            while (issued < stages && issued < steps) load_act();
+            grid_dependency_wait();
+            while (i < steps && !*abort_flag) {
+                if (i >= issued) {
+                    if (!bar_wait(empty + 8 * ai.slot, ai.phase ^ 1u)) {
+                        *abort_flag = 1u;
+                        break;
                     }
-                    load_t();
+                    load_act();
                 }
-                while (i < issued) load_t();  // a stage that the loop left without its t gets it, so that its phase ends
-                wait_out(full, stages, issued, gi);
+                load_mid();
             }
+            while (i < issued) load_mid();  // a stage that the loop left without its t or u gets it, so that its phase ends
+            wait_out(full, stages, issued, ai);
+            if (kX) wait_out(ufull, stages, i, mi);
         }
     } else if (warp == 1) {
         const bool leader = elect();
-        const uint32_t three = idesc_bf16(128, 3 * p.rp, 1, 1), two = idesc_bf16(128, 2 * p.rp, 1, 1);
-        constexpr uint32_t kPiece = kX ? kChunkX : kChunk;
-        const uint64_t a0 = smem_desc_sw128(smem_u32(smem), kPiece, 1024);
-        const uint64_t b0 = smem_desc_sw128(smem_u32(smem) + (kX ? 2 * kOutTileX : kOutA), kPiece, 1024);
+        constexpr uint32_t kMnMajor = kX ? 0 : 1;  // A: grad_h as it lies, x from TMEM
+        const uint32_t three = idesc_bf16(128, 3 * p.rp, kMnMajor, 1), two = idesc_bf16(128, 2 * p.rp, kMnMajor, 1);
+        uint64_t a = smem_desc_sw128(base, kChunk, 1024), b = smem_desc_sw128(base + kAct, kChunk, 1024);
+        uint32_t at = tmem + kTmemA;
+        Ring r, t, d;
         int i = 0;
-        Ring r, d;
-        for (; i < steps; ++i, r.next(stages)) {
-            const bool first = i % kDrain == 0;
-            if (first && i > 0) {
-                if (!mbar_wait(drained, d.phase)) break;
+        bool ok = true;
+        while (ok && i < steps) {
+            const int end = steps - i < kDrain ? steps : i + kDrain;
+            if (i > 0) {
+                ok = bar_wait(drained, d.phase);
+                if (!ok) break;
                 d.next(1);
             }
-            if (!mbar_wait(&full[r.slot], r.phase)) break;
-            __syncwarp();
-            tc_fence_after();
-            const uint64_t a = a0 + r.slot * (stage / 16), b = b0 + r.slot * (stage / 16);
-            const uint32_t more = first ? 0u : 1u;
-            if (leader) {
+            uint32_t more = 0u;
+            for (; i < end; ++i) {
+                ok = kX ? bar_wait(ready + 8 * t.slot, t.phase) : bar_wait(full + 8 * r.slot, r.phase);
+                if (!ok) break;
+                __syncwarp();
+                tc_fence_after();
+                if (leader) {
 #pragma unroll
-                for (uint32_t kk = 0; kk < kTok / 16; ++kk) {
-                    const uint64_t bd = b + 128 * kk;
+                    for (uint32_t kk = 0; kk < 4; ++kk) {
+                        if (kX) {
+                            mma_bf16_ts(tmem, at + 8 * kk, b + 128 * kk, three, kk > 0 ? 1u : more);
+                            // lo is 2^-8 of hi: its product with the third term is below the fp32 sums
+                            mma_bf16_ts(tmem, at + 8 * kk + 32, b + 128 * kk, two, 1u);
+                        } else {
 #pragma unroll
-                    for (uint32_t half = 0; half < 2; ++half) {
-                        const uint64_t ad = a + 2 * half * (kPiece / 16) + 128 * kk;
-                        mma_bf16_ss(tmem + 256 * half, ad, bd, three, kk > 0 ? 1u : more);
-                        // lo is 2^-8 of hi: its product with the third term is below the fp32 sums
-                        if (kX) mma_bf16_ss(tmem + 256 * half, ad + kOutTileX / 16, bd, two, 1u);
+                            for (uint32_t half = 0; half < 2; ++half)
+                                mma_bf16_ss(tmem + 256 * half, a + 2 * half * (kChunk / 16) + 128 * kk, b + 128 * kk, three, kk > 0 ? 1u : more);
+                        }
                     }
+                    commit(empty + 8 * r.slot);
                 }
-                mma_commit(&empty[r.slot]);
-                if (i % kDrain == kDrain - 1 || i + 1 == steps) mma_commit(done);
+                more = 1u;
+                a += stage / 16;
+                b += stage / 16;
+                r.next(stages);
+                if (r.slot == 0) {
+                    a -= stages * (stage / 16);
+                    b -= stages * (stage / 16);
+                }
+                if (kX) {
+                    t.next(4);
+                    at = tmem + kTmemA + 64 * t.slot;
+                }
             }
-            __syncwarp();
+            if (leader) commit(done);  // also when left early: the warps wait for it all the same
         }
-        if (i < steps) {  // left early: the warps wait for it all the same
-            *abort_flag = 1u;
-            if (leader) mma_commit(done);
-        }
+        if (!ok) *abort_flag = 1u;
         wait_out(empty, stages, i, r);
     } else if (warp == kOutThreads / 32 - 1) {
         const int64_t blocks = p.k / kBlock, blk0 = col0 / kBlock;
-        // a group: a token's four blocks at one of the batch's four steps
-        if (kX && !load_absmax<kBatch * kTok>(steps, reinterpret_cast<uint64_t *>(absmax), afull, aempty, lane, [&](int i, int e, int &count) {
-                const int64_t m = tok(i + e / kTok) + static_cast<int64_t>(e % kTok);
-                const bool live = i + e / kTok < steps && m < p.M;
-                count = live ? static_cast<int>(blocks - blk0 < 4 ? blocks - blk0 : 4) : 0;
-                return p.absmax + (live ? m : 0) * blocks + blk0;
-            }))
+        // a group: a token's two blocks at one of the batch's four steps; kept as [step][block][token]
+        if (kX && !load_absmax<2, kBatch * kK>(
+                      steps, afull, aempty, lane,
+                      [&](int i, int e, int &count) {
+                          const int64_t m = tok(i + e / kK) + static_cast<int64_t>(e % kK);
+                          const bool live = i + e / kK < steps && m < p.M;
+                          count = live ? static_cast<int>(blocks - blk0 < 2 ? blocks - blk0 : 2) : 0;
+                          return p.absmax + (live ? m : 0) * blocks + blk0;
+                      },
+                      [&](int batch, int e, uint64_t v) {
+#pragma unroll
+                          for (int q = 0; q < 2; ++q)
+                              absmax[((batch * kBatch + e / kK) * 2 + q) * kK + e % kK] = static_cast<uint16_t>(v >> (16 * q));
+                      }))
             *abort_flag = 1u;
     } else if (!kX) {
         for (int i = 0; i < steps; i += kDrain)
@@ -772,42 +840,99 @@ __device__ __forceinline__ void outer_tc(const CUtensorMap *act, const CUtensorM
                 break;
             }
     } else {
-        // token of the step, block of the tile; the group takes every fourth step, always in the same slot
-        const int id = (threadIdx.x - 64) & 127, group = (warp - 2) >> 2;
-        const uint32_t row = id & 31u, blk = id >> 5;
-        const int64_t col = col0 + 64 * static_cast<int64_t>(blk);
-        const uint32_t from = smem_u32(codes) + group * (kOutTileX / 2) + blk * (kChunkX / 2) + row * 64u;
-        const uint32_t to = smem_u32(smem) + group * stage + blk * kChunkX + row * 128u;
-        Ring b;
-        uint32_t phase = 0;
+        // The group takes every fourth step; the warp has the 32 lanes of its quarter, two segments of 16 columns of one
+        // block. ldmatrix with .trans, on pairs of codes, gives thread (g, t) columns 2 g and 2 g + 1 of the tokens 2 t and
+        // 2 t + 1: as bf16 pairs of tokens, the lanes g and g + 8 of a 16 x 128b store. So column 2 g (+ 1) of a segment lies
+        // in lane g (g + 8). A x that goes through shared memory as hi and lo instead is written and read once more, 8 B a
+        // code, and that bounds the kernel.
+        const uint32_t blk = quarter >> 1, seg = 2 * (quarter & 1u);
+        const uint32_t swz = ((static_cast<uint32_t>(lane) >> 1) & 3u) << 4;  // this lane points ldmatrix at tokens lane, lane + 32
+        const uint32_t from = base + blk * (kOutCodes / 2) + lane * 64u;
+        const uint32_t to = tmem + kTmemA + 64 * group + ((quarter * 32u) << 16);
+        Ring r, b;
+        for (int e = 0; e < group; ++e) r.next(stages);
+        Ring last = r;  // the stage of the group's step before
         bool ok = true;
-        for (int i = group; i < steps; i += 4, phase ^= 1u) {
-            ok = mbar_wait(&afull[b.slot], b.phase) && mbar_wait(&cfull[group], phase) && (i < 4 || mbar_wait(&empty[group], phase ^ 1u));
+        int drains = 0;  // of the segments of kDrain steps so far
+        for (int i = group; i < steps; i += 4) {
+            // A segment is drained as soon as it is seen to be done, at the latest after the group's first step of the next
+            // one: that step's slot is free by then, the MMAs that would read it wait for the drain.
+            if (drains < i / kDrain && __all_sync(0xffffffffu, bar_test(done, drains & 1))) {
+                ok = drain(static_cast<uint32_t>(drains));
+                ++drains;
+            }
+            ok = ok && bar_wait(afull + 8 * b.slot, b.phase) && bar_wait(full + 8 * r.slot, r.phase) && (i < 4 || bar_wait(empty + 8 * last.slot, last.phase));
             if (!ok) break;
-            const float a = __uint_as_float(static_cast<uint32_t>(absmax[((b.slot * kBatch + group) * kTok + row) * 4 + blk]) << 16);
-            convert_block<true, kOutTileX, kDrop>(from, row, a, p.drop,
-                                                  p.drop.offset + static_cast<uint64_t>((tok(i) + static_cast<int64_t>(row)) * p.k + col), to);
-            fence_proxy_async_smem();
+            __syncwarp();
+            tc_fence_after();
+            const uint32_t here = from + r.slot * stage;
+            if (kDrop) {  // the step's codes, half a row of a block (32) a thread and turn, masked in place
+#pragma unroll 1
+                for (uint32_t e = quarter * 32u + lane; e < 256; e += 128) {
+                    const uint32_t token = e & 63u, part = e >> 6;
+                    const uint32_t at = base + r.slot * stage + (part >> 1) * (kOutCodes / 2) + token * 64u;
+                    const uint64_t e0 = p.drop.offset + static_cast<uint64_t>((tok(i) + static_cast<int64_t>(token)) * p.k + col0 + 32 * part);
+#pragma unroll
+                    for (uint32_t c = 0; c < 2; ++c) {
+                        const uint32_t addr = at + (((2 * (part & 1u) + c) ^ ((token >> 1) & 3u)) << 4);
+                        const uint32_t keep = dropout_keep_bits(p.drop, e0 + 16 * c, 16);
+                        uint32_t w[4];
+                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr) : "memory");
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) w[q] &= keep_bytes(keep >> (4 * q));
+                        sts128(addr, w);
+                    }
+                }
+                fence_proxy_async_smem();  // the stage's next load overwrites what was stored here
+                asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
+            }
+            const uint16_t *am = absmax + ((b.slot * kBatch + group) * 2 + blk) * kK + 2 * (lane & 3);
+#pragma unroll
+            for (uint32_t half = 0; half < 2; ++half) {  // 32 tokens each
+                __nv_bfloat162 f[4];  // a / 128 of the token pairs
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    f[e] = __hmul2(as_bf2(*reinterpret_cast<const uint32_t *>(am + 32 * half + 8 * e)), __float2bfloat162_rn(0.0078125f));
+#pragma unroll
+                for (uint32_t sgm = 0; sgm < 2; ++sgm) {
+                    uint32_t w[4], hi[8], lw[8];
+                    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                 : "r"(here + half * 2048u + (((seg + sgm) << 4) ^ swz))
+                                 : "memory");
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const __nv_bfloat162 v = code_pair(c == 0 ? w[e] : w[e] >> 8);
+                            const __nv_bfloat162 top = __hmul2(v, f[e]);
+                            hi[2 * e + c] = bf2(top);
+                            lw[2 * e + c] = bf2(__hfma2(v, f[e], __hneg2(top)));
+                        }
+                    tmem_st_16x128b_x4(to + ((16u * sgm) << 16) + 16 * half, hi);
+                    tmem_st_16x128b_x4(to + ((16u * sgm) << 16) + 16 * half + 32, lw);
+                }
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            ok = bar_wait(ufull + 8 * r.slot, r.phase);  // for the MMA thread, which then waits once
+            if (!ok) break;
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&cempty[group]);
-                mbar_arrive(&full[group]);
-                mbar_arrive(&aempty[b.slot]);
+                bar_arrive(ready + 8 * group);
+                bar_arrive(aempty + 8 * b.slot);
             }
             b.next(kBatches);
-            // The drain of the segment before comes after the group's first step of this one: its slot is free by then, the
-            // MMAs that would read it wait for the drain.
-            if (i >= kDrain && i % kDrain < 4) {
-                ok = drain(static_cast<uint32_t>(i / kDrain - 1));
+            last = r;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) r.next(stages);
+            if (drains < i / kDrain) {
+                ok = drain(static_cast<uint32_t>(drains));
+                ++drains;
                 if (!ok) break;
             }
         }
-        // drains that no step of this group followed, and the last one
-        if (ok && steps > 0) {
-            const int last = (steps - 1) / kDrain;
-            if (last > 0 && last * kDrain + group >= steps) ok = drain(static_cast<uint32_t>(last - 1));
-            ok = ok && drain(static_cast<uint32_t>(last));
-        }
+        for (; ok && drains * kDrain < steps; ++drains) ok = drain(static_cast<uint32_t>(drains));
         if (!ok) *abort_flag = 1u;
     }
     __syncthreads();  // every load has landed: the ring is free for the sums
@@ -816,9 +941,10 @@ __device__ __forceinline__ void outer_tc(const CUtensorMap *act, const CUtensorM
     float *red = reinterpret_cast<float *>(smem);
     if (warp >= 2 && warp < 2 + kOutWarps) {
         const bool ok = !*abort_flag;
-        const int c = static_cast<int>(h * 128 + quarter * 32 + lane);
+        const int l = kX ? (lane & 16) + ((lane & 7) << 1) + ((lane >> 3) & 1) : lane;  // column of the lane
+        const int c = static_cast<int>(h * 128 + quarter * 32) + l;
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < kJs; ++b) {
             const int j = 16 * (jb0 + 2 * b);
             if (j >= p.rp) break;
             if (!ok) {
@@ -845,7 +971,7 @@ __device__ __forceinline__ void outer_tc(const CUtensorMap *act, const CUtensorM
     }
     // each rank adds up its share, four neighbouring values of the result per thread
     const int js = p.r - p.j0 < p.rp ? p.r - p.j0 : p.rp;  // a multiple of 8
-    const int inner = (kX ? kOutCols : js) / 4, items = inner * (kX ? js : kOutCols);
+    const int inner = (kX ? kCols : js) / 4, items = inner * (kX ? js : kCols);
     const int e0 = static_cast<int>(static_cast<int64_t>(items) * rank / ranks);
     const int e1 = static_cast<int>(static_cast<int64_t>(items) * (rank + 1) / ranks);
     float *out = kX ? p.grad_A : p.grad_B;
@@ -884,9 +1010,9 @@ k_outer_tc(const __grid_constant__ CUtensorMap tm_gh, const __grid_constant__ CU
            const __grid_constant__ CUtensorMap tm_t, const __grid_constant__ CUtensorMap tm_u, const TcArgs p) {
     extern __shared__ uint8_t raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + out_ring(p.chunks) + kOutAbsmax);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kOutRoom + kOutAbsmax);
     const uint32_t rank = cta_rank(), ranks = cta_ranks();
-    const int64_t tile = blockIdx.x / ranks, tiles_gh = (p.n + kOutCols - 1) / kOutCols;
+    const int64_t tile = blockIdx.x / ranks, tiles_gh = (p.n + kColsGh - 1) / kColsGh;
     if (tile < tiles_gh)
         outer_tc<false, false>(&tm_gh, &tm_t, p, smem, bars, tile, rank, ranks);
     else
@@ -944,6 +1070,47 @@ cudaError_t launch_clusters(K kern, dim3 grid, int threads, size_t smem, int ran
     return e;
 }
 
+// Clusters of 1 .. 8 CTAs, one on an SM, that are resident at once: of the current context, kept per host thread.
+struct Fits {
+    uint64_t ctx = 0;
+    int dev = -1;
+    int clusters[9];
+};
+
+cudaError_t cluster_fits(const Fits **out) {
+    static thread_local Fits kept;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t ctx = current_context_id();
+    if (kept.dev != dev || kept.ctx != ctx || ctx == 0) {
+        for (int c = 1; c <= 8; ++c) {
+            e = resident_clusters(reinterpret_cast<const void *>(k_outer_tc<false>), kOutThreads, c, kOutSmem, &kept.clusters[c]);
+            if (e != cudaSuccess) return e;
+        }
+        kept.dev = dev;
+        kept.ctx = ctx;
+    }
+    *out = &kept;
+    return cudaSuccess;
+}
+
+// The cluster size with the least waves x (steps of a CTA + what a CTA costs besides, in steps).
+int cluster_size(const Fits &fits, int per_sm, int64_t tiles, int64_t steps, int64_t besides) {
+    int best = 1;
+    int64_t least = 0;
+    for (int c = 1; c <= 8 && c <= steps; ++c) {
+        const int64_t fit = static_cast<int64_t>(per_sm) * fits.clusters[c];
+        if (fit <= 0) continue;
+        const int64_t cost = (tiles + fit - 1) / fit * ((steps + c - 1) / c + besides);
+        if (least == 0 || cost < least) {
+            least = cost;
+            best = c;
+        }
+    }
+    return best;
+}
+
 int pass_rank(int r) { return r >= 64 ? 64 : (r + 15) / 16 * 16; }
 int pass_chunks(int rp) { return (3 * rp + 63) / 64; }
 
@@ -958,40 +1125,34 @@ bool act8_grads_tc_supported(int64_t M, int64_t n, int r) { return n % 8 == 0 &&
 cudaError_t launch_act8_grads_tc(const int8_t *codes, const uint16_t *absmax, const uint16_t *gh, int64_t M, int64_t n,
                                  int64_t k, const uint16_t *A, const uint16_t *B, int r, float s,
                                  const DropoutArgs &drop, float *grad_A, float *grad_B, void *ws, cudaStream_t st) {
-    int sms = 148;
-    cudaError_t e = device_sm_count(&sms);
-    if (e != cudaSuccess) return e;
+    cudaError_t e = cudaSuccess;
     TcArgs p{absmax, M, n, k, r, 0, 0, 0, s * (128.0f / 127.0f), grad_A, grad_B, static_cast<uint16_t *>(ws), nullptr, drop};
     p.u = reinterpret_cast<uint16_t *>(static_cast<char *>(ws) + act8_grads_tc_workspace_bytes(M, r) / 2);
-    CUtensorMap tm_gh, tm_codes, tm_codes32, tm_A, tm_B, tm_t, tm_u;
-    if (!make_map(&tm_gh, gh, M, n, false) || !make_map(&tm_codes, codes, M, k, true) || !make_map(&tm_codes32, codes, M, k, true, kTokX) || !make_map(&tm_B, B, n, r, false))
+    CUtensorMap tm_gh, tm_codes, tm_A, tm_B, tm_t, tm_u;
+    if (!make_map(&tm_gh, gh, M, n, false) || !make_map(&tm_codes, codes, M, k, true) || !make_map(&tm_B, B, n, r, false))
         return cudaErrorInvalidValue;
-    const int64_t tok = (M + kDownTile - 1) / kDownTile, tiles = (n + kOutCols - 1) / kOutCols + (k + kOutCols - 1) / kOutCols;
+    const int64_t tok = (M + kDownTile - 1) / kDownTile, tiles = (n + kColsGh - 1) / kColsGh + (k + kColsX - 1) / kColsX;
     if (tok > (int64_t(1) << 28) || tiles > (int64_t(1) << 28)) return cudaErrorInvalidConfiguration;
     const int64_t pieces = (n > k ? n : k) / kK, steps = (M + kK - 1) / kK;  // of 64; both sides of a cluster have some
-    // CTAs of a cluster: as many as keep one wave (two CTAs of the first kernel fit an SM, one of the second)
-    auto ranks = [](int64_t tiles, int64_t room, int64_t most) {
-        int c = 1;
-        while (c < 8 && 2 * c * tiles <= room && 2 * c <= most) c *= 2;
-        return c;
-    };
-    int rd = ranks(2 * tok, 2 * sms, pieces);
-    while (rd < 8 && pieces / rd > 64) rd *= 2;  // a wide side: more CTAs than one wave, evener and with shorter sums
-    const int ro = ranks(tiles, sms, steps);
+    const bool masked = drop.thr != 0u;
+    const Fits *fits = nullptr;
+    e = cluster_fits(&fits);
+    if (e != cudaSuccess) return e;
+    // two CTAs of the first kernel share an SM
+    const int rd = cluster_size(*fits, 2, 2 * tok, pieces, 10), ro = cluster_size(*fits, 1, tiles, steps, 12);
     for (p.j0 = 0; p.j0 < r; p.j0 += 64) {
         p.rp = pass_rank(r - p.j0);
         p.chunks = pass_chunks(p.rp);
-        if (!make_map(&tm_A, A, r, k, false, static_cast<uint32_t>(p.rp)) || !make_map(&tm_t, p.t, M, 64 * p.chunks, false) || !make_map(&tm_u, p.u, M, 64 * p.chunks, false, kTokX)) return cudaErrorInvalidValue;
+        if (!make_map(&tm_A, A, r, k, false, static_cast<uint32_t>(p.rp)) || !make_map(&tm_t, p.t, M, 64 * p.chunks, false) || !make_map(&tm_u, p.u, M, 64 * p.chunks, false)) return cudaErrorInvalidValue;
         const dim3 gd(static_cast<unsigned>(tok * rd), 2, 1), go(static_cast<unsigned>(tiles * ro), 1, 1);
-        const size_t so = 1024 + out_ring(p.chunks) + kOutAbsmax + 512;
-        if (drop.thr != 0u) {
+        if (masked) {
             e = launch_clusters(k_down_tc<true>, gd, kDownThreads, kDownSmem, rd, false, tm_gh, tm_codes, tm_A, tm_B, p, st);
             if (e == cudaSuccess)
-                e = launch_clusters(k_outer_tc<true>, go, kOutThreads, so, ro, true, tm_gh, tm_codes32, tm_t, tm_u, p, st);
+                e = launch_clusters(k_outer_tc<true>, go, kOutThreads, kOutSmem, ro, true, tm_gh, tm_codes, tm_t, tm_u, p, st);
         } else {
             e = launch_clusters(k_down_tc<false>, gd, kDownThreads, kDownSmem, rd, false, tm_gh, tm_codes, tm_A, tm_B, p, st);
             if (e == cudaSuccess)
-                e = launch_clusters(k_outer_tc<false>, go, kOutThreads, so, ro, true, tm_gh, tm_codes32, tm_t, tm_u, p, st);
+                e = launch_clusters(k_outer_tc<false>, go, kOutThreads, kOutSmem, ro, true, tm_gh, tm_codes, tm_t, tm_u, p, st);
         }
         if (e != cudaSuccess) return e;
     }
