@@ -108,7 +108,7 @@ def load(path: str | None = None):
         lib.qn_act8_sizes.argtypes = [i64, i64, sz, sz]
         lib.act8_quantize.argtypes = [P, A8, P]
         lib.act8_dequantize.argtypes = [A8, P, P]
-        lib.qlora_lora_grads_act8_workspace_size.argtypes = [i64, ctypes.c_int, sz]
+        lib.qlora_lora_grads_act8_workspace_size.argtypes = [i64, i64, ctypes.c_int, sz]
         lib.qlora_lora_grads_act8.argtypes = [A8, P, i64, P, P, ctypes.c_int, ctypes.c_float, D, P, P, P,
                                               ctypes.c_size_t, P]
         lib.swiglu_act8_fwd.argtypes = [P, P, P, A8, A8, P]
@@ -553,9 +553,10 @@ def act8_dequantize(a: Act8, out: torch.Tensor | None = None, stream=None) -> to
     return out
 
 
-def lora_grads_act8_workspace_size(M: int, r: int) -> int:
+def lora_grads_act8_workspace_size(M: int, n_out: int, r: int) -> int:
     v = ctypes.c_size_t()
-    _check(load().qlora_lora_grads_act8_workspace_size(M, r, ctypes.byref(v)), "qlora_lora_grads_act8_workspace_size")
+    _check(load().qlora_lora_grads_act8_workspace_size(M, n_out, r, ctypes.byref(v)),
+           "qlora_lora_grads_act8_workspace_size")
     return v.value
 
 
@@ -583,7 +584,7 @@ def qlora_lora_grads_act8(x: Act8, grad_h: torch.Tensor, A: torch.Tensor, B: tor
     else:
         _expect(grad_B, "grad_B", f32, (n, r), dev)
     if workspace is None:
-        workspace = torch.empty(lora_grads_act8_workspace_size(M, r), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(lora_grads_act8_workspace_size(M, n, r), dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
     d = None if dropout is None else ctypes.byref(_dropout_struct(dropout))

@@ -80,5 +80,39 @@ __device__ __forceinline__ void decode4(uint32_t w, float (&f)[4]) {
         f[i] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7540u + static_cast<uint32_t>(i))) - 8388736.0f;
 }
 
+// 8 neighbouring bf16 from column c of a row of n on, zeros past its end, of a matrix whose rows lie on any 2-byte
+// boundary and that starts on a 16-byte one: cut out of the two aligned words around them. `end` is the end of the matrix,
+// which no word may pass.
+__device__ __forceinline__ uint4 load_row8(const uint16_t *row, int64_t c, int64_t n, const uint16_t *end) {
+    if (c >= n) return make_uint4(0u, 0u, 0u, 0u);
+    const uint16_t *p = row + c;
+    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;  // bytes, even
+    const uint16_t *a = p - off / 2;
+    uint32_t w[8];
+    const bool low = a + 8 <= end, high = a + 16 <= end;
+    const uint4 v0 = low ? ld_ro_v4(a) : make_uint4(0u, 0u, 0u, 0u), v1 = high ? ld_ro_v4(a + 8) : make_uint4(0u, 0u, 0u, 0u);
+    w[0] = v0.x; w[1] = v0.y; w[2] = v0.z; w[3] = v0.w;
+    w[4] = v1.x; w[5] = v1.y; w[6] = v1.z; w[7] = v1.w;
+    if (!high) {  // the last words of the matrix: value by value
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t lo = a + 2 * e < end ? ld_ro_u16(a + 2 * e) : 0u, hi = a + 2 * e + 1 < end ? ld_ro_u16(a + 2 * e + 1) : 0u;
+            w[e] = lo | hi << 16;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 6; ++e) w[e] = (off & 8u) ? w[e + 2] : w[e];
+#pragma unroll
+    for (int e = 0; e < 5; ++e) w[e] = (off & 4u) ? w[e + 1] : w[e];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = __funnelshift_r(w[e], w[e + 1], (off & 2u) * 8u);
+    if (c + 8 > n) {  // the next row's values
+        const uint32_t left = static_cast<uint32_t>(n - c);
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e) w[e] &= (2 * e < left ? 0xffffu : 0u) | (2 * e + 1 < left ? 0xffff0000u : 0u);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 }  // namespace act8
 }  // namespace qn

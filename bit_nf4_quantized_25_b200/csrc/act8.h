@@ -25,16 +25,15 @@ cudaError_t launch_swiglu_act8_bwd(const int8_t *gate_codes, const uint16_t *gat
                                    cudaStream_t st);
 
 // Adapter gradients (fp32) with the input in 8 bits: grad_A (r x k), grad_B (n x r); M, n, k > 0. The workspace
-// holds t = x A^T and u = grad_h B in fp32.
-size_t act8_grads_workspace_bytes(int64_t M, int r);
+// holds t = x A^T and u = grad_h B.
+size_t act8_grads_workspace_bytes(int64_t M, int64_t n, int r);
 cudaError_t launch_act8_grads(const int8_t *codes, const uint16_t *absmax, const uint16_t *gh, int64_t M, int64_t n,
                               int64_t k, const uint16_t *A, const uint16_t *B, int r, float s, const DropoutArgs &drop,
                               float *grad_A, float *grad_B, void *ws, cudaStream_t st);
 
-// The same on the 5th-generation tensor cores, for what act8_grads_tc_supported: rows of grad_h and of B that
-// TMA can read.
-size_t act8_grads_tc_workspace_bytes(int64_t M, int r);
-bool act8_grads_tc_supported(int64_t M, int64_t n, int r);
+// The same on the 5th-generation tensor cores, for long batches. The workspace also holds copies of grad_h and B with
+// padded rows where TMA cannot read theirs (n % 8, r % 8).
+size_t act8_grads_tc_workspace_bytes(int64_t M, int64_t n, int r);
 cudaError_t launch_act8_grads_tc(const int8_t *codes, const uint16_t *absmax, const uint16_t *gh, int64_t M, int64_t n,
                                  int64_t k, const uint16_t *A, const uint16_t *B, int r, float s,
                                  const DropoutArgs &drop, float *grad_A, float *grad_B, void *ws, cudaStream_t st);

@@ -10,13 +10,11 @@
 // in fp32: to the 64-feature partial sums of t, and to u before the second product.
 //
 // Results are fp32 and meant to be as good: t and u are kept in fp32 between the two kernels and enter
-// the second product as three bf16 terms (24 bits). All sums are fp32 in a fixed order.
+// the second product as three bf16 terms (24 bits). All sums are fp32 in a fixed order, those of more than a few MMAs
+// by fp32 additions: the tensor core cuts off what it adds to an accumulator instead of rounding it.
 //
-// These are the kernels for any rank and any width of grad_h, and for short batches; act8_grads_tc.cu has those for long
-// ones. Two kernels, each reading the codes and grad_h once, straight into registers; the second finds in L2
-// what fits there.
-//   k_down   t and u: a warp has 32 tokens, a CTA 128, a cluster splits the features; the adapter's factors go
-//            through shared memory in pieces of 64 features.
+// These are the kernels for short batches; act8_grads_tc.cu has those for long ones. Two kernels, straight into registers:
+//   k_down   t and u: a CTA has 32 tokens, its eight warps and a cluster's CTAs split the features.
 //   k_outer  the two products over tokens: a warp has 64 columns of x or grad_h and every j, a CTA 256 columns
 //            and two token streams, a cluster splits the tokens. The A operand wants neighbouring tokens of one
 //            column in a register: a lane loads 8 columns of 4 tokens and pairs them with byte permutes.
@@ -86,91 +84,71 @@ __device__ __forceinline__ uint2 drop_codes(uint2 v, const DropoutArgs &d, uint6
     return make_uint2(v.x & bytes(keep), v.y & bytes(keep >> 4));
 }
 
-// 8 neighbouring bf16 of a row of grad_h from column c on; zeros past its end. Rows that are not 16-byte
-// aligned (n % 8 != 0) are read element by element.
+// 8 neighbouring bf16 of a row of grad_h from column c on; zeros past its end. kAligned: rows are 16-byte aligned.
 template <bool kAligned>
-__device__ __forceinline__ uint4 load_gh(const uint16_t *row, int64_t c, int64_t n) {
-    if constexpr (kAligned) {
+__device__ __forceinline__ uint4 load_gh(const uint16_t *row, int64_t c, int64_t n, const uint16_t *end) {
+    if constexpr (kAligned)
         return c < n ? ld_nc_v4(row + c) : make_uint4(0u, 0u, 0u, 0u);
-    } else {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t lo = c + 2 * i < n ? ld_ro_u16(row + c + 2 * i) : 0u;
-            const uint32_t hi = c + 2 * i + 1 < n ? ld_ro_u16(row + c + 2 * i + 1) : 0u;
-            w[i] = lo | (hi << 16);
-        }
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    }
+    else
+        return act8::load_row8(row, c, n, end);
 }
 
 // ------------------------------------------------------------------------ t and u
 
-constexpr int kDownWarps = 4;
+constexpr int kDownWarps = 8;
 constexpr int kDownThreads = 32 * kDownWarps;
-constexpr int kDownTokens = 32 * kDownWarps;
-constexpr int kPiece = 64;       // features per step
-constexpr int kARow = 96;        // bf16 per row of the piece of A: 64 and padding (192 B: two rows' 64-byte
-                                 // reads of a quarter warp fall on different banks)
+constexpr int kDownTokens = 32;
+constexpr int kPiece = 64;  // features per step of a warp
 
+// NT neighbouring bf16 from p on, of which `count` exist, as NT / 2 pairs (NT = 1: one value).
 template <int NT>
-struct DownSmem {
-    static constexpr int kBRow = NT == 1 ? 8 : 8 * NT + 8;  // bf16 per row of the piece of B: an odd number of 16-byte
-                                                            // units, so 8 rows in a row are free of conflicts
-    static constexpr int kPieceBytes = 8 * NT * kARow * 2 > kPiece * kBRow * 2 ? 8 * NT * kARow * 2 : kPiece * kBRow * 2;
-    static constexpr int kRedRow = 8 * NT + 1;
-    static constexpr int kRed = kDownTokens * kRedRow * 4;
-    static constexpr int kBytes = 2 * kPieceBytes > kRed ? 2 * kPieceBytes : kRed;
-};
-
-// The order of the features inside 32 is free as long as both operands agree: lane t has the 8 features
-// 8 t .. 8 t + 7, two for each half of two MMAs. Row c of a piece of B goes where the 8 rows of one 8 x 8
-// matrix of ldmatrix are neighbours.
-__device__ __forceinline__ int b_slot(int c) { return (c & 32) | ((c & 7) << 2) | ((c >> 3) & 3); }
-
-template <int NT, bool kX>
-__device__ __forceinline__ void stage_factor(const GradArgs &p, uint16_t *buf, int64_t c0) {
-    if (kX) {
-        // rows j of A, 64 features each
-        for (int i = threadIdx.x; i < 8 * NT * 8; i += kDownThreads) {
-            const int j = i >> 3, seg = i & 7;
-            const bool ok = p.j0 + j < p.r;
-            const uint16_t *src = ok ? p.A + static_cast<int64_t>(p.j0 + j) * p.k + c0 + 8 * seg : p.A;
-            stream::cp_async16_zfill(stream::saddr(buf + j * kARow + 8 * seg), src, ok ? 16u : 0u);
-        }
-    } else if ((p.r & 7) == 0) {
-        for (int i = threadIdx.x; i < kPiece * NT; i += kDownThreads) {
-            const int c = i / NT, seg = i % NT;
-            const bool ok = c0 + c < p.n && p.j0 + 8 * seg < p.r;
-            const uint16_t *src = ok ? p.B + (c0 + c) * p.r + p.j0 + 8 * seg : p.B;
-            stream::cp_async16_zfill(stream::saddr(buf + b_slot(c) * DownSmem<NT>::kBRow + 8 * seg), src, ok ? 16u : 0u);
+__device__ __forceinline__ void load_js(const uint16_t *p, int count, bool vec, uint32_t (&w)[(NT + 1) / 2]) {
+    if (vec && count >= NT) {
+        if constexpr (NT == 8) {
+            const uint4 v = ld_ro_v4(p);
+            w[0] = v.x;
+            w[1] = v.y;
+            w[2] = v.z;
+            w[3] = v.w;
+        } else if constexpr (NT == 4) {
+            const uint2 v = ld_ro_v2(p);
+            w[0] = v.x;
+            w[1] = v.y;
+        } else if constexpr (NT == 2) {
+            w[0] = ld_ro_u32(p);
+        } else {
+            w[0] = ld_ro_u16(p);
         }
     } else {
-        for (int i = threadIdx.x; i < kPiece * 8 * NT; i += kDownThreads) {
-            const int c = i / (8 * NT), j = i % (8 * NT);
-            const bool ok = c0 + c < p.n && p.j0 + j < p.r;
-            buf[b_slot(c) * DownSmem<NT>::kBRow + j] = ok ? ld_ro_u16(p.B + (c0 + c) * p.r + p.j0 + j) : 0;
+#pragma unroll
+        for (int i = 0; i < (NT + 1) / 2; ++i) {
+            const uint32_t lo = 2 * i < count ? ld_ro_u16(p + 2 * i) : 0u;
+            const uint32_t hi = NT > 1 && 2 * i + 1 < count ? ld_ro_u16(p + 2 * i + 1) : 0u;
+            w[i] = lo | hi << 16;
         }
     }
-    stream::cp_async_commit();
 }
 
-template <int NT, bool kX, bool kDrop, bool kAligned>
-__device__ __forceinline__ void down(const GradArgs &p, uint8_t *smem, int64_t tile, uint32_t rank, uint32_t ranks) {
-    using S = DownSmem<NT>;
+// Everything comes straight into registers: with few tokens the factors are most of what is read, each once per 32 tokens.
+// The order of the features in a step is free as long as both operands agree, and so is the order of the columns j:
+//   x       lane t has the features 8 t .. 8 t + 7 of 32, two for each half of two MMAs; A's rows give the same pairs
+//   grad_h  lane t has the features 4 t .. 4 t + 3 of 16; of B it loads those rows, NT neighbouring j, and pairs rows by byte
+//           permutes
+// Column g of the MMA's tile nt is j = NT g + nt.
+template <int NT, bool kX, bool kDrop>
+__device__ __forceinline__ void down(const GradArgs &p, float *red, int64_t tile, uint32_t rank, uint32_t ranks) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    auto buf = [&](int b) { return reinterpret_cast<uint16_t *>(smem + b * S::kPieceBytes); };
-    const int64_t m0 = tile * kDownTokens + 32 * warp;
+    const int64_t m0 = tile * kDownTokens;
     const int64_t width = kX ? p.k : p.n, pieces = (width + kPiece - 1) / kPiece;
-    const int64_t lo = pieces * rank / ranks, hi = pieces * (rank + 1) / ranks;
-    int64_t row[4];  // this lane's tokens: g, g + 8, g + 16, g + 24 of the warp's 32
+    int64_t row[4];  // this lane's tokens: g, g + 8, g + 16, g + 24
     bool live[4];
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
-        const int64_t m = m0 + g + 8 * h;
-        live[h] = m < p.M;
-        row[h] = live[h] ? m : 0;
+        live[h] = m0 + g + 8 * h < p.M;
+        row[h] = live[h] ? m0 + g + 8 * h : 0;
     }
+    const int js = p.r - p.j0 < 8 * NT ? p.r - p.j0 : 8 * NT;  // columns of this pass
+    const bool vec = p.r % NT == 0;
 
     float acc[2][NT][4];
 #pragma unroll
@@ -178,112 +156,107 @@ __device__ __forceinline__ void down(const GradArgs &p, uint8_t *smem, int64_t t
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) acc[mt][nt][0] = acc[mt][nt][1] = acc[mt][nt][2] = acc[mt][nt][3] = 0.0f;
 
-    uint4 v[2][4];       // grad_h: [32 features][token]
-    uint2 q[2][4];       // codes
-    uint32_t top[4];     // absmax of the piece
-    auto load = [&](int64_t c) {
-        const int64_t c0 = c * kPiece + 8 * t;
+    for (int64_t c = rank * kDownWarps + warp; c < pieces; c += static_cast<int64_t>(ranks) * kDownWarps) {
+        float d[2][NT][4];
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            if (kX) {
-                const int8_t *src = p.codes + row[h] * p.k + c0;
+        for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-                for (int sub = 0; sub < 2; ++sub) q[sub][h] = live[h] ? ld_nc_v2(src + 32 * sub) : make_uint2(0u, 0u);
-                top[h] = live[h] ? ld_ro_u16(p.absmax + row[h] * (p.k / kBlock) + c) : 0u;
-            } else {
+            for (int nt = 0; nt < NT; ++nt) d[mt][nt][0] = d[mt][nt][1] = d[mt][nt][2] = d[mt][nt][3] = 0.0f;
+        float sc[4];
+        if (kX) {
+            uint2 q[2][4];
+            const int64_t c0 = c * kPiece + 8 * t;
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
 #pragma unroll
                 for (int sub = 0; sub < 2; ++sub)
-                    v[sub][h] = live[h] ? load_gh<kAligned>(p.gh + row[h] * p.n, c0 + 32 * sub, p.n)
-                                        : make_uint4(0u, 0u, 0u, 0u);
+                    q[sub][h] = live[h] ? ld_nc_v2(p.codes + row[h] * p.k + c0 + 32 * sub) : make_uint2(0u, 0u);
+                const uint32_t top = live[h] ? ld_ro_u16(p.absmax + row[h] * (p.k / kBlock) + c) : 0u;
+                sc[h] = __uint_as_float(top << 16) * (1.0f / 127.0f);
             }
-        }
-    };
-
-    if (lo < hi) {
-        stage_factor<NT, kX>(p, buf(0), lo * kPiece);
-        load(lo);
-    }
-    for (int64_t c = lo; c < hi; ++c) {
-        const int b = static_cast<int>((c - lo) & 1);
-        uint32_t a[2][4][4];  // [32 features][token][pair]
-        float sc[4];
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
 #pragma unroll
             for (int sub = 0; sub < 2; ++sub) {
-                if (kX) {
+                uint32_t a[4][4];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
                     uint2 w = q[sub][h];
                     if (kDrop && live[h])
-                        w = drop_codes(w, p.drop, p.drop.offset + static_cast<uint64_t>(row[h] * p.k + c * kPiece + 32 * sub + 8 * t));
-                    a[sub][h][0] = codes_to_bf16(__byte_perm(w.x, 0u, 0x4140));
-                    a[sub][h][1] = codes_to_bf16(__byte_perm(w.x, 0u, 0x4342));
-                    a[sub][h][2] = codes_to_bf16(__byte_perm(w.y, 0u, 0x4140));
-                    a[sub][h][3] = codes_to_bf16(__byte_perm(w.y, 0u, 0x4342));
-                } else {
-                    a[sub][h][0] = v[sub][h].x;
-                    a[sub][h][1] = v[sub][h].y;
-                    a[sub][h][2] = v[sub][h].z;
-                    a[sub][h][3] = v[sub][h].w;
+                        w = drop_codes(w, p.drop, p.drop.offset + static_cast<uint64_t>(row[h] * p.k + c0 + 32 * sub));
+                    a[h][0] = codes_to_bf16(__byte_perm(w.x, 0u, 0x4140));
+                    a[h][1] = codes_to_bf16(__byte_perm(w.x, 0u, 0x4342));
+                    a[h][2] = codes_to_bf16(__byte_perm(w.y, 0u, 0x4140));
+                    a[h][3] = codes_to_bf16(__byte_perm(w.y, 0u, 0x4342));
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const int j = NT * g + nt;
+                    const uint4 f = j < js ? ld_ro_v4(p.A + static_cast<int64_t>(p.j0 + j) * p.k + c0 + 32 * sub) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt) {
+                        mma_16816(d[mt][nt], a[2 * mt][0], a[2 * mt + 1][0], a[2 * mt][1], a[2 * mt + 1][1], f.x, f.y);
+                        mma_16816(d[mt][nt], a[2 * mt][2], a[2 * mt + 1][2], a[2 * mt][3], a[2 * mt + 1][3], f.z, f.w);
+                    }
                 }
             }
-            if (kX) sc[h] = __uint_as_float(top[h] << 16) * (1.0f / 127.0f);
-        }
-        if (c + 1 < hi) {
-            stage_factor<NT, kX>(p, buf(b ^ 1), (c + 1) * kPiece);
-            load(c + 1);
-            stream::cp_async_wait_n<1>();
         } else {
-            stream::cp_async_wait_n<0>();
-        }
-        __syncthreads();
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float d[2][4];
+            for (int h = 0; h < 4; ++h) sc[h] = 1.0f;
+            const bool pairs = p.n % 4 == 0;
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
+            for (int ks = 0; ks < 4; ++ks) {
+                const int64_t c0 = c * kPiece + 16 * ks + 4 * t;
+                uint2 v[4];
+                uint32_t w[4][(NT + 1) / 2];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) d[mt][i] = kX ? 0.0f : acc[mt][nt][i];
+                for (int h = 0; h < 4; ++h) {
+                    const uint16_t *src = p.gh + row[h] * p.n + c0;
+                    v[h] = make_uint2(0u, 0u);
+                    if (pairs) {
+                        if (live[h] && c0 < p.n) v[h] = ld_ro_v2(src);
+                    } else if (live[h]) {
+                        uint32_t e[4];
 #pragma unroll
-            for (int sub = 0; sub < 2; ++sub) {
-                uint32_t f[4];
-                if (kX) {
-                    const uint4 w = *reinterpret_cast<const uint4 *>(buf(b) + (8 * nt + g) * kARow + 32 * sub + 8 * t);
-                    f[0] = w.x;
-                    f[1] = w.y;
-                    f[2] = w.z;
-                    f[3] = w.w;
-                } else {
-                    const int i = lane & 7;
-                    const int slot = 32 * sub + (2 * (lane >> 3) + (i & 1)) * 4 + (i >> 1);
-                    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                                 : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
-                                 : "r"(stream::saddr(buf(b) + slot * S::kBRow + 8 * nt)));
+                        for (int q = 0; q < 4; ++q) e[q] = c0 + q < p.n ? ld_ro_u16(src + q) : 0u;
+                        v[h] = make_uint2(e[0] | e[1] << 16, e[2] | e[3] << 16);
+                    }
                 }
 #pragma unroll
-                for (int mt = 0; mt < 2; ++mt) {
-                    const uint32_t(&x0)[4] = a[sub][2 * mt], (&x1)[4] = a[sub][2 * mt + 1];
-                    mma_16816(d[mt], x0[0], x1[0], x0[1], x1[1], f[0], f[1]);
-                    mma_16816(d[mt], x0[2], x1[2], x0[3], x1[3], f[2], f[3]);
+                for (int q = 0; q < 4; ++q)
+                    load_js<NT>(p.B + (c0 + q) * p.r + p.j0 + NT * g, c0 + q < p.n ? js - NT * g : 0, vec, w[q]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const uint32_t sel = (nt & 1) ? 0x7632 : 0x5410;
+                    const uint32_t b0 = __byte_perm(w[0][nt / 2], w[1][nt / 2], sel), b1 = __byte_perm(w[2][nt / 2], w[3][nt / 2], sel);
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt)
+                        mma_16816(d[mt][nt], v[2 * mt].x, v[2 * mt + 1].x, v[2 * mt].y, v[2 * mt + 1].y, b0, b1);
                 }
             }
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    acc[mt][nt][i] = kX ? __fmaf_rn(sc[2 * mt + (i >> 1)], d[mt][i], acc[mt][nt][i]) : d[mt][i];
         }
-        __syncthreads();  // the buffer is refilled in the next step
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[mt][nt][i] = __fmaf_rn(sc[2 * mt + (i >> 1)], d[mt][nt][i], acc[mt][nt][i]);
     }
 
-    // the cluster's partial sums, added in rank order; each rank writes its share of the tile
-    float *red = reinterpret_cast<float *>(smem);
+    // the warps' sums in order, then the cluster's in rank order; each rank writes its share of the tile
+    constexpr int kRow = 8 * NT + 1, kTile = kDownTokens * kRow;
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                red[(32 * warp + 16 * mt + g + 8 * (i >> 1)) * S::kRedRow + 8 * nt + 2 * t + (i & 1)] = acc[mt][nt][i];
+                red[warp * kTile + (16 * mt + g + 8 * (i >> 1)) * kRow + NT * (2 * t + (i & 1)) + nt] = acc[mt][nt][i];
+    __syncthreads();
+    for (int e = threadIdx.x; e < kTile; e += kDownThreads) {
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kDownWarps; ++w) v += red[w * kTile + e];
+        red[e] = v;
+    }
     if (ranks > 1) {
         stream::cluster_arrive_release();
         stream::cluster_wait_acquire();
@@ -298,7 +271,7 @@ __device__ __forceinline__ void down(const GradArgs &p, uint8_t *smem, int64_t t
         const int i = e & 3, l = (e >> 2) & 31, nt = (e >> 7) % NT, m16 = e / (128 * NT);
         const int64_t mg = tile * (kDownTokens / 16) + m16;
         if (mg * 16 >= p.M || jt0 + nt >= jt_all) continue;
-        const float *src = red + (16 * m16 + 4 * (l & 3) + i) * S::kRedRow + 8 * nt + (l >> 2);
+        const float *src = red + (16 * m16 + 4 * (l & 3) + i) * kRow + 8 * nt + (l >> 2);
         float sum = 0.0f;
         if (ranks > 1)
             for (uint32_t k = 0; k < ranks; ++k) sum += ld_cluster(src, k);
@@ -313,15 +286,15 @@ __device__ __forceinline__ void down(const GradArgs &p, uint8_t *smem, int64_t t
 }
 
 // grid (ranks * token tiles, 2): y = 0 takes u from grad_h, y = 1 t from the codes.
-template <int NT, bool kDrop, bool kAligned>
+template <int NT, bool kDrop>
 __global__ void __launch_bounds__(kDownThreads) k_down(const GradArgs p) {
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ __align__(16) float red[];
     const uint32_t rank = cluster_rank(), ranks = cluster_size();
     const int64_t tile = blockIdx.x / ranks;
     if (blockIdx.y == 0)
-        down<NT, false, false, kAligned>(p, smem, tile, rank, ranks);
+        down<NT, false, false>(p, red, tile, rank, ranks);
     else
-        down<NT, true, kDrop, true>(p, smem, tile, rank, ranks);
+        down<NT, true, kDrop>(p, red, tile, rank, ranks);
 }
 
 // -------------------------------------------------------------- products over tokens
@@ -371,7 +344,7 @@ __device__ __forceinline__ void outer(const GradArgs &p, float *red, int64_t til
                 q[i] = m < p.M ? ld_nc_v2(p.codes + m * p.k + col) : make_uint2(0u, 0u);
                 top[i] = m < p.M ? ld_ro_u16(p.absmax + m * (p.k / kBlock) + col0 / kBlock) : 0u;
             } else {
-                v[i] = m < p.M ? load_gh<kAligned>(p.gh + m * p.n, col, p.n) : make_uint4(0u, 0u, 0u, 0u);
+                v[i] = m < p.M ? load_gh<kAligned>(p.gh + m * p.n, col, p.n, p.gh + p.M * p.n) : make_uint4(0u, 0u, 0u, 0u);
             }
         }
     };
@@ -426,11 +399,18 @@ __device__ __forceinline__ void outer(const GradArgs &p, float *red, int64_t til
             }
             uint32_t part[3][2];
             split(w, part);
+            float d[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.0f;
 #pragma unroll
             for (int term = 0; term < 3; ++term)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    mma_16816(acc[i][nt], a[i][0], a[i][1], a[i][2], a[i][3], part[term][0], part[term][1]);
+                    mma_16816(d[i], a[i][0], a[i][1], a[i][2], a[i][3], part[term][0], part[term][1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][nt][e] += d[i][e];
         }
     }
 
@@ -524,11 +504,11 @@ int split_ranks(int64_t tiles, int64_t want, int64_t most) {
 template <int NT, bool kDrop, bool kAligned>
 cudaError_t launch_pass(const GradArgs &p, int sms, cudaStream_t st) {
     const int64_t tok = (p.M + kDownTokens - 1) / kDownTokens;
-    const int64_t pieces = (p.n > p.k ? p.n : p.k) / kPiece;
-    int ranks = split_ranks(2 * tok, 3 * sms, pieces > 1 ? pieces : 1);
+    const int64_t rounds = ((p.n > p.k ? p.n : p.k) + kPiece * kDownWarps - 1) / (kPiece * kDownWarps);
+    int ranks = split_ranks(2 * tok, 2 * sms, rounds);
     if (tok * ranks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    cudaError_t e = launch_clusters(k_down<NT, kDrop, kAligned>, dim3(static_cast<unsigned>(tok * ranks), 2, 1), kDownThreads,
-                                    DownSmem<NT>::kBytes, ranks, p, st);
+    cudaError_t e = launch_clusters(k_down<NT, kDrop>, dim3(static_cast<unsigned>(tok * ranks), 2, 1), kDownThreads,
+                                    static_cast<size_t>(kDownWarps) * kDownTokens * (8 * NT + 1) * 4, ranks, p, st);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (p.n + kOutCols - 1) / kOutCols + (p.k + kOutCols - 1) / kOutCols;
     ranks = split_ranks(tiles, NT > 4 ? sms : 2 * sms, (p.M + 16 * kTokWarps - 1) / (16 * kTokWarps));
@@ -546,19 +526,21 @@ cudaError_t launch_nt(const GradArgs &p, int sms, cudaStream_t st) {
 
 // Batches from this many tokens on go to the tcgen05 kernels.
 constexpr int64_t kTcTokens = 128;
+// Workspace of these kernels: t and u.
+size_t few_bytes(int64_t M, int r) {
+    return 2 * sizeof(float) * static_cast<size_t>((M + 15) / 16) * 16 * static_cast<size_t>((r + 7) / 8 * 8);
+}
 
 }  // namespace
 
-size_t act8_grads_workspace_bytes(int64_t M, int r) {
-    const size_t one = static_cast<size_t>((M + 15) / 16) * 16 * static_cast<size_t>((r + 7) / 8 * 8) * sizeof(float);
-    const size_t here = 2 * ((one + 255) & ~size_t(255)), tc = act8_grads_tc_workspace_bytes(M, r);
-    return here > tc ? here : tc;
+size_t act8_grads_workspace_bytes(int64_t M, int64_t n, int r) {
+    return M >= kTcTokens ? act8_grads_tc_workspace_bytes(M, n, r) : few_bytes(M, r);
 }
 
 cudaError_t launch_act8_grads(const int8_t *codes, const uint16_t *absmax, const uint16_t *gh, int64_t M, int64_t n,
                               int64_t k, const uint16_t *A, const uint16_t *B, int r, float s, const DropoutArgs &drop,
                               float *grad_A, float *grad_B, void *ws, cudaStream_t st) {
-    if (M >= kTcTokens && act8_grads_tc_supported(M, n, r))
+    if (M >= kTcTokens)
         return launch_act8_grads_tc(codes, absmax, gh, M, n, k, A, B, r, s, drop, grad_A, grad_B, ws, st);
     int sms = 148;
     cudaError_t e = device_sm_count(&sms);

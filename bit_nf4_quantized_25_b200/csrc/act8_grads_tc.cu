@@ -266,27 +266,35 @@ __device__ __forceinline__ bool feed(int steps, int &ci, Ring &c, int slots, uin
 // and `put(batch, group, values)` stores them. In the converting warps themselves the loads' latency showed in every fourth step.
 constexpr int kBatch = 4, kBatches = 3;
 
-// kN (2 or 4) neighbouring ones at p, of which `count` exist.
-template <int kN>
-__device__ __forceinline__ uint64_t load_few(const uint16_t *p, int count) {
-    if (count >= kN && (reinterpret_cast<uintptr_t>(p) & (2u * kN - 1u)) == 0)
-        return kN == 4 ? __ldg(reinterpret_cast<const unsigned long long *>(p)) : ld_ro_u32(p);
-    uint64_t v = 0;
-#pragma unroll 1
-    for (int i = 0; i < count && i < kN; ++i) v |= static_cast<uint64_t>(ld_ro_u16(p + i)) << (16 * i);
-    return v;
-}
-
 template <int kN, int kGroups, typename At, typename Put>
 __device__ __forceinline__ bool load_absmax(int steps, uint32_t afull, uint32_t aempty, int lane, At &&at, Put &&put) {
     Ring b;
     for (int i = 0; i < steps; i += kBatch, b.next(kBatches)) {
+        // all loads of whole, aligned groups before the first use, then the values of the others
         uint64_t v[kGroups / 32];
+        bool rest = false;
 #pragma unroll
         for (int g = 0; g < kGroups / 32; ++g) {
             int count;
             const uint16_t *p = at(i, 32 * g + lane, count);
-            v[g] = load_few<kN>(p, count);
+            v[g] = 0;
+            if (count >= kN && (reinterpret_cast<uintptr_t>(p) & (2u * kN - 1u)) == 0)
+                v[g] = kN == 4 ? __ldg(reinterpret_cast<const unsigned long long *>(p)) : ld_ro_u32(p);
+            else if (count > 0)
+                rest = true;
+        }
+        if (rest) {
+#pragma unroll
+            for (int g = 0; g < kGroups / 32; ++g) {
+                int count;
+                const uint16_t *p = at(i, 32 * g + lane, count);
+                if (count >= kN && (reinterpret_cast<uintptr_t>(p) & (2u * kN - 1u)) == 0) continue;
+                uint32_t w[kN];
+#pragma unroll
+                for (int e = 0; e < kN; ++e) w[e] = e < count ? ld_ro_u16(p + e) : 0u;
+#pragma unroll
+                for (int e = 0; e < kN; ++e) v[g] |= static_cast<uint64_t>(w[e]) << (16 * e);
+            }
         }
         if (i >= kBatches * kBatch && !bar_wait(aempty + 8 * b.slot, b.phase ^ 1u)) return false;
 #pragma unroll
@@ -319,7 +327,9 @@ static_assert(2 * kDownTile * kDownRedRow * 4 <= kDownRing, "");
 constexpr uint32_t kDownAbsmax = kBatches * kBatch * kDownTile * 2;
 constexpr size_t kDownSmem = 1024 + kDownRing + kDownAbsmax + 512;
 
-template <bool kX, bool kDrop>
+// kBlocks: 16-column blocks of t or u that a thread can hold, 2 (rp <= 32) or 4. With 4, 80 registers a thread (two CTAs on
+// an SM) do not hold everything and some spill; at that rank grad_h, not x, sets the pace.
+template <bool kX, bool kDrop, int kBlocks>
 __device__ __forceinline__ void down_tc(const CUtensorMap *act, const CUtensorMap *factor, const TcArgs &p, uint8_t *smem,
                                         uint64_t *bars, int64_t tile, uint32_t rank, uint32_t ranks) {
     constexpr int kStages = kX ? kDownStagesX : kDownStagesGh;
@@ -374,15 +384,15 @@ __device__ __forceinline__ void down_tc(const CUtensorMap *act, const CUtensorMa
     // Warps 2 .. 9 have 32 lanes (tokens) of the accumulators each, of every other one.
     const uint32_t quarter = static_cast<uint32_t>(warp & 3);
     const int group = (warp - 2) >> 2;
-    float sum[4][16];
+    float sum[kBlocks][16];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int e = 0; e < kBlocks; ++e)
 #pragma unroll
         for (int q = 0; q < 16; ++q) sum[e][q] = 0.0f;
     // adds the accumulator in columns from d on, times a
     auto add = [&](uint32_t d, float a) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < kBlocks; ++e)
             if (16 * e < p.rp) {
                 uint32_t v[16];
                 tmem_ld16(tmem + ((quarter * 32u) << 16) + d + 16 * e, v);
@@ -549,7 +559,7 @@ __device__ __forceinline__ void down_tc(const CUtensorMap *act, const CUtensorMa
         float4 *dst = reinterpret_cast<float4 *>(red + (group * kDownTile + quarter * 32 + lane) * kDownRedRow);
         const float nan = __uint_as_float(0x7fc00000u);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < kBlocks; ++e)
             if (16 * e < p.rp) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
@@ -601,7 +611,7 @@ __device__ __forceinline__ void down_tc(const CUtensorMap *act, const CUtensorMa
 }
 
 // grid (ranks * token tiles, 2): y = 0 takes u from grad_h, y = 1 t from the codes.
-template <bool kDrop>
+template <bool kDrop, int kBlocks>
 __global__ void __launch_bounds__(kDownThreads, 2)
 k_down_tc(const __grid_constant__ CUtensorMap tm_gh, const __grid_constant__ CUtensorMap tm_codes,
           const __grid_constant__ CUtensorMap tm_A, const __grid_constant__ CUtensorMap tm_B, const TcArgs p) {
@@ -611,31 +621,34 @@ k_down_tc(const __grid_constant__ CUtensorMap tm_gh, const __grid_constant__ CUt
     const uint32_t rank = cta_rank(), ranks = cta_ranks();
     const int64_t tile = blockIdx.x / ranks;
     if (blockIdx.y == 0)
-        down_tc<false, false>(&tm_gh, &tm_B, p, smem, bars, tile, rank, ranks);
+        down_tc<false, false, kBlocks>(&tm_gh, &tm_B, p, smem, bars, tile, rank, ranks);
     else
-        down_tc<true, kDrop>(&tm_codes, &tm_A, p, smem, bars, tile, rank, ranks);
+        down_tc<true, kDrop, kBlocks>(&tm_codes, &tm_A, p, smem, bars, tile, rank, ranks);
 }
 
 // ------------------------------------------------------------------------ products over tokens
 
 constexpr int kColsGh = 256, kColsX = 128;
 constexpr int kOutWarps = 16;  // converters: four groups that take steps in turn, each with its slot of TMEM
-constexpr int kOutThreads = 96 + 32 * kOutWarps;  // with the producer, the MMA and the absmax warp
+constexpr int kDrainWarps = 4;  // of x
+constexpr int kOutThreads = 96 + 32 * (kOutWarps + kDrainWarps);  // with the producer, the MMA and the absmax warp
 constexpr uint32_t kTmemA = 256;  // x: columns of A, 32 hi and 32 lo for each group; the accumulator has at most 192
 constexpr uint32_t kOutA = 4 * kChunk;      // 64 tokens x 256 columns of grad_h
 constexpr uint32_t kOutCodes = kK * kColsX;  // bytes of codes of a step
 constexpr int kMaxStages = 8;
 constexpr uint32_t kOutRoom = 200 * 1024;
 
+constexpr int kOutRowX = kColsX + 4;  // floats per row j of the sums of x, behind the stages
+constexpr uint32_t kOutSums = 64 * kOutRowX * 4;
+
 // Stages that fit for a row of t or u of `chunks` pieces: grad_h or codes, and t or u.
 __host__ __device__ constexpr int out_stages(bool x, int chunks) {
-    const int fit = static_cast<int>(kOutRoom / ((x ? kOutCodes : kOutA) + static_cast<uint32_t>(chunks) * kChunk));
+    const int fit = static_cast<int>((x ? kOutRoom - kOutSums : kOutRoom) / ((x ? kOutCodes : kOutA) + static_cast<uint32_t>(chunks) * kChunk));
     return fit > kMaxStages ? kMaxStages : fit;
 }
 constexpr uint32_t kOutAbsmax = kBatches * kBatch * 2 * kK * 2;
-constexpr int kOutRowX = kColsX + 4;  // floats per row j of the sums of x
 constexpr int kOutRowGh = 68;         // floats per column of grad_h of its sums
-static_assert(64 * kOutRowX * 4 <= kOutRoom && kColsGh * kOutRowGh * 4 <= kOutRoom, "");
+static_assert(kColsGh * kOutRowGh * 4 <= kOutRoom && kOutSums % 16 == 0, "");
 constexpr size_t kOutSmem = 1024 + kOutRoom + kOutAbsmax + 512;
 
 template <bool kX, bool kDrop>
@@ -643,14 +656,16 @@ __device__ __forceinline__ void outer_tc(const CUtensorMap *act, const CUtensorM
                                          uint64_t *bars, int64_t tile, uint32_t rank, uint32_t ranks) {
     constexpr int kCols = kX ? kColsX : kColsGh;
     constexpr uint32_t kAct = kX ? kOutCodes : kOutA;
-    // Steps between two drains of the accumulators into registers: the tensor core cuts off what it adds instead of
-    // rounding it, and a chain of 256 MMAs would be off by 1e-5.
-    constexpr int kDrain = kX ? 8 : 16;
+    // Steps between two drains of the accumulators: the tensor core cuts off what it adds instead of rounding it, and a
+    // chain of 256 MMAs would be off by 1e-5. Up to rank 32 there is TMEM for two accumulators in turn, which the MMAs do
+    // not wait for, so drains are twice as frequent.
+    const int turns = p.rp <= 32 ? 2 : 1;
+    const int every = (kX ? 8 : 16) / turns;
     const int stages = out_stages(kX, p.chunks);
     const uint32_t stage = kAct + p.chunks * kChunk;  // codes or grad_h, then u or t
     const uint32_t base = smem_u32(smem), full = smem_u32(bars), empty = full + 8 * kMaxStages, ready = empty + 8 * kMaxStages, ufull = ready + 32;
-    const uint32_t afull = ufull + 8 * kMaxStages, aempty = afull + 8 * kBatches, done = aempty + 8 * kBatches, drained = done + 8;
-    uint32_t *slot = reinterpret_cast<uint32_t *>(bars + 3 * kMaxStages + 4 + 2 * kBatches + 2);
+    const uint32_t afull = ufull + 8 * kMaxStages, aempty = afull + 8 * kBatches, done = aempty + 8 * kBatches, drained = done + 16;
+    uint32_t *slot = reinterpret_cast<uint32_t *>(bars + 3 * kMaxStages + 4 + 2 * kBatches + 4);
     volatile uint32_t *abort_flag = slot + 1;
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const int64_t width = kX ? p.k : p.n;
@@ -673,8 +688,10 @@ __device__ __forceinline__ void outer_tc(const CUtensorMap *act, const CUtensorM
             bar_init(afull + 8 * s, 1);
             bar_init(aempty + 8 * s, kOutWarps);
         }
-        bar_init(done, 1);             // the MMAs up to a drain are done
-        bar_init(drained, kOutWarps);  // the warps have read the accumulators
+        for (int s = 0; s < 2; ++s) {
+            bar_init(done + 8 * s, 1);                                // the MMAs up to a drain are done
+            bar_init(drained + 8 * s, kX ? kDrainWarps : kOutWarps);  // the warps have read the accumulators
+        }
         *abort_flag = 0u;
         fence_barrier_init();
     }
@@ -691,39 +708,49 @@ __device__ __forceinline__ void outer_tc(const CUtensorMap *act, const CUtensorM
     tc_fence_after();
     const uint32_t tmem = *slot;
 
-    // Warps 2 .. 17 drain 32 lanes (columns) of an accumulator each: of grad_h's two, every other 16 of the columns j; of
-    // x's, 16 columns j.
+    // Warps drain 32 lanes (columns) of an accumulator each: of grad_h's two, warps 2 .. 17 every other 16 of the columns j;
+    // of x's, the last four warps all of them. (Were x's drained by its converters, the MMAs would wait for a conversion.)
     const uint32_t quarter = static_cast<uint32_t>(warp & 3);
     const int group = (warp - 2) >> 2;
     const uint32_t h = kX ? 0u : static_cast<uint32_t>(group & 1);
-    const int jb0 = kX ? group : group >> 1;
-    constexpr int kJs = kX ? 1 : 2;
-    float sum[kJs][16];
+    const int jb0 = group >> 1;
+    float *red = reinterpret_cast<float *>(smem + (kX ? kOutRoom - kOutSums : 0));
+    float sum[2][16];  // of grad_h; those of x are in shared memory, there is no room for 64 of a thread in registers
 #pragma unroll
-    for (int b = 0; b < kJs; ++b)
+    for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int c = 0; c < 16; ++c) sum[b][c] = 0.0f;
-    auto drain = [&](uint32_t nth) -> bool {
-        if (!bar_wait(done, nth & 1u)) return false;
+    // column of x in the warp's 32 that lies in this lane (see the converters)
+    const int lane_x = (lane & 16) + ((lane & 7) << 1) + ((lane >> 3) & 1);
+    Ring turn;
+    auto drain = [&](bool first) -> bool {
+        if (!bar_wait(done + 8 * turn.slot, turn.phase)) return false;
         tc_fence_after();
-        const uint32_t d = tmem + 256 * h + ((quarter * 32u) << 16);
+        const uint32_t d = tmem + 256 * h + 128 * turn.slot + ((quarter * 32u) << 16);
 #pragma unroll
-        for (int b = 0; b < kJs; ++b) {
-            const int j = 16 * (jb0 + 2 * b);
+        for (int b = 0; b < (kX ? 4 : 2); ++b) {
+            const int j = kX ? 16 * b : 16 * (jb0 + 2 * b);
             if (j < p.rp) {
                 uint32_t v0[16], v1[16], v2[16];
                 tmem_ld16(d + j, v0);
                 tmem_ld16(d + p.rp + j, v1);
                 tmem_ld16(d + 2 * p.rp + j, v2);
                 tmem_ld_wait();
+                float *to = red + j * kOutRowX + static_cast<int>(quarter * 32) + lane_x;
 #pragma unroll
-                for (int c = 0; c < 16; ++c)
-                    sum[b][c] += __uint_as_float(v0[c]) + (__uint_as_float(v1[c]) + __uint_as_float(v2[c]));
+                for (int c = 0; c < 16; ++c) {
+                    const float v = __uint_as_float(v0[c]) + (__uint_as_float(v1[c]) + __uint_as_float(v2[c]));
+                    if (kX)
+                        to[c * kOutRowX] = first ? v : to[c * kOutRowX] + v;
+                    else
+                        sum[b][c] += v;
+                }
             }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) bar_arrive(drained);
+        if (lane == 0) bar_arrive(drained + 8 * turn.slot);
+        turn.next(turns);
         return true;
     };
 
@@ -772,12 +799,12 @@ __device__ __forceinline__ void outer_tc(const CUtensorMap *act, const CUtensorM
         int i = 0;
         bool ok = true;
         while (ok && i < steps) {
-            const int end = steps - i < kDrain ? steps : i + kDrain;
-            if (i > 0) {
-                ok = bar_wait(drained, d.phase);
+            const int end = steps - i < every ? steps : i + every;
+            if (i >= turns * every) {
+                ok = bar_wait(drained + 8 * d.slot, d.phase ^ 1u);
                 if (!ok) break;
-                d.next(1);
             }
+            const uint32_t acc = tmem + 128 * d.slot;
             uint32_t more = 0u;
             for (; i < end; ++i) {
                 ok = kX ? bar_wait(ready + 8 * t.slot, t.phase) : bar_wait(full + 8 * r.slot, r.phase);
@@ -788,13 +815,13 @@ __device__ __forceinline__ void outer_tc(const CUtensorMap *act, const CUtensorM
 #pragma unroll
                     for (uint32_t kk = 0; kk < 4; ++kk) {
                         if (kX) {
-                            mma_bf16_ts(tmem, at + 8 * kk, b + 128 * kk, three, kk > 0 ? 1u : more);
+                            mma_bf16_ts(acc, at + 8 * kk, b + 128 * kk, three, kk > 0 ? 1u : more);
                             // lo is 2^-8 of hi: its product with the third term is below the fp32 sums
-                            mma_bf16_ts(tmem, at + 8 * kk + 32, b + 128 * kk, two, 1u);
+                            mma_bf16_ts(acc, at + 8 * kk + 32, b + 128 * kk, two, 1u);
                         } else {
 #pragma unroll
                             for (uint32_t half = 0; half < 2; ++half)
-                                mma_bf16_ss(tmem + 256 * half, a + 2 * half * (kChunk / 16) + 128 * kk, b + 128 * kk, three, kk > 0 ? 1u : more);
+                                mma_bf16_ss(acc + 256 * half, a + 2 * half * (kChunk / 16) + 128 * kk, b + 128 * kk, three, kk > 0 ? 1u : more);
                         }
                     }
                     commit(empty + 8 * r.slot);
@@ -812,11 +839,12 @@ __device__ __forceinline__ void outer_tc(const CUtensorMap *act, const CUtensorM
                     at = tmem + kTmemA + 64 * t.slot;
                 }
             }
-            if (leader) commit(done);  // also when left early: the warps wait for it all the same
+            if (leader) commit(done + 8 * d.slot);  // also when left early: the warps wait for it all the same
+            d.next(turns);
         }
         if (!ok) *abort_flag = 1u;
         wait_out(empty, stages, i, r);
-    } else if (warp == kOutThreads / 32 - 1) {
+    } else if (warp == 2 + kOutWarps) {
         const int64_t blocks = p.k / kBlock, blk0 = col0 / kBlock;
         // a group: a token's two blocks at one of the batch's four steps; kept as [step][block][token]
         if (kX && !load_absmax<2, kBatch * kK>(
@@ -833,9 +861,9 @@ __device__ __forceinline__ void outer_tc(const CUtensorMap *act, const CUtensorM
                               absmax[((batch * kBatch + e / kK) * 2 + q) * kK + e % kK] = static_cast<uint16_t>(v >> (16 * q));
                       }))
             *abort_flag = 1u;
-    } else if (!kX) {
-        for (int i = 0; i < steps; i += kDrain)
-            if (*abort_flag || !drain(static_cast<uint32_t>(i / kDrain))) {
+    } else if (!kX || warp > 2 + kOutWarps) {
+        for (int i = 0; i < steps && (kX || warp < 2 + kOutWarps); i += every)
+            if (*abort_flag || !drain(i == 0)) {
                 *abort_flag = 1u;
                 break;
             }
@@ -853,15 +881,8 @@ __device__ __forceinline__ void outer_tc(const CUtensorMap *act, const CUtensorM
         for (int e = 0; e < group; ++e) r.next(stages);
         Ring last = r;  // the stage of the group's step before
         bool ok = true;
-        int drains = 0;  // of the segments of kDrain steps so far
         for (int i = group; i < steps; i += 4) {
-            // A segment is drained as soon as it is seen to be done, at the latest after the group's first step of the next
-            // one: that step's slot is free by then, the MMAs that would read it wait for the drain.
-            if (drains < i / kDrain && __all_sync(0xffffffffu, bar_test(done, drains & 1))) {
-                ok = drain(static_cast<uint32_t>(drains));
-                ++drains;
-            }
-            ok = ok && bar_wait(afull + 8 * b.slot, b.phase) && bar_wait(full + 8 * r.slot, r.phase) && (i < 4 || bar_wait(empty + 8 * last.slot, last.phase));
+            ok = bar_wait(afull + 8 * b.slot, b.phase) && bar_wait(full + 8 * r.slot, r.phase) && (i < 4 || bar_wait(empty + 8 * last.slot, last.phase));
             if (!ok) break;
             __syncwarp();
             tc_fence_after();
@@ -926,41 +947,29 @@ __device__ __forceinline__ void outer_tc(const CUtensorMap *act, const CUtensorM
             last = r;
 #pragma unroll
             for (int e = 0; e < 4; ++e) r.next(stages);
-            if (drains < i / kDrain) {
-                ok = drain(static_cast<uint32_t>(drains));
-                ++drains;
-                if (!ok) break;
-            }
         }
-        for (; ok && drains * kDrain < steps; ++drains) ok = drain(static_cast<uint32_t>(drains));
         if (!ok) *abort_flag = 1u;
     }
     __syncthreads();  // every load has landed: the ring is free for the sums
 
-    // the sums to shared memory: of x a row of columns per j, of grad_h a row of j per column, as they go out
-    float *red = reinterpret_cast<float *>(smem);
-    if (warp >= 2 && warp < 2 + kOutWarps) {
-        const bool ok = !*abort_flag;
-        const int l = kX ? (lane & 16) + ((lane & 7) << 1) + ((lane >> 3) & 1) : lane;  // column of the lane
-        const int c = static_cast<int>(h * 128 + quarter * 32) + l;
+    // the sums of grad_h to shared memory, a row of j per column, as they go out; those of x are there, a row of columns
+    // per j
+    const bool ok = !*abort_flag && steps > 0;
+    if (!kX && ok && warp >= 2 && warp < 2 + kOutWarps) {
+        const int c = static_cast<int>(h * 128 + quarter * 32) + lane;
 #pragma unroll
-        for (int b = 0; b < kJs; ++b) {
+        for (int b = 0; b < 2; ++b) {
             const int j = 16 * (jb0 + 2 * b);
             if (j >= p.rp) break;
-            if (!ok) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) sum[b][e] = __uint_as_float(0x7fc00000u);
-            }
-            if (kX) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) red[(j + e) * kOutRowX + c] = sum[b][e];
-            } else {
-#pragma unroll
-                for (int e = 0; e < 16; e += 4)
-                    *reinterpret_cast<float4 *>(red + c * kOutRowGh + j + e) =
-                        make_float4(sum[b][e], sum[b][e + 1], sum[b][e + 2], sum[b][e + 3]);
-            }
+            for (int e = 0; e < 16; e += 4)
+                *reinterpret_cast<float4 *>(red + c * kOutRowGh + j + e) =
+                    make_float4(sum[b][e], sum[b][e + 1], sum[b][e + 2], sum[b][e + 3]);
         }
+    }
+    if (!ok) {  // no steps: zeros; a wait ran out: NaN
+        const float v = *abort_flag ? __uint_as_float(0x7fc00000u) : 0.0f;
+        for (int e = threadIdx.x; e < (kX ? 64 * kOutRowX : kColsGh * kOutRowGh); e += kOutThreads) red[e] = v;
     }
     __syncwarp();
     if (ranks > 1) {
@@ -970,12 +979,12 @@ __device__ __forceinline__ void outer_tc(const CUtensorMap *act, const CUtensorM
         __syncthreads();
     }
     // each rank adds up its share, four neighbouring values of the result per thread
-    const int js = p.r - p.j0 < p.rp ? p.r - p.j0 : p.rp;  // a multiple of 8
-    const int inner = (kX ? kCols : js) / 4, items = inner * (kX ? js : kCols);
+    const int js = p.r - p.j0 < p.rp ? p.r - p.j0 : p.rp;
+    const int inner = (kX ? kCols : js + 3) / 4, items = inner * (kX ? js : kCols);
     const int e0 = static_cast<int>(static_cast<int64_t>(items) * rank / ranks);
     const int e1 = static_cast<int>(static_cast<int64_t>(items) * (rank + 1) / ranks);
     float *out = kX ? p.grad_A : p.grad_B;
-    const bool vec = (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
+    const bool vec = (reinterpret_cast<uintptr_t>(out) & 15u) == 0 && (kX || p.r % 4 == 0);
     for (int e = e0 + threadIdx.x; e < e1; e += kOutThreads) {
         const int o = e / inner, q = 4 * (e - o * inner);
         const int j = kX ? o : q, c = kX ? q : o;
@@ -990,7 +999,8 @@ __device__ __forceinline__ void outer_tc(const CUtensorMap *act, const CUtensorM
             *reinterpret_cast<float4 *>(dst) = make_float4(v[0], v[1], v[2], v[3]);
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) dst[i] = v[i];
+            for (int i = 0; i < 4; ++i)
+                if (kX || j + i < js) dst[i] = v[i];
         }
     }
     __syncwarp();
@@ -1070,6 +1080,21 @@ cudaError_t launch_clusters(K kern, dim3 grid, int threads, size_t smem, int ran
     return e;
 }
 
+// rows x cols bf16 to rows of up8(cols), zeros behind: 8 values of a row per thread, cut out of the aligned words around them.
+__global__ void __launch_bounds__(256) k_pad(const uint16_t *src, int64_t rows, int64_t cols, int64_t chunks, uint16_t *to) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, row = i / chunks, c = (i - row * chunks) * 8;
+    if (row >= rows) return;
+    *reinterpret_cast<uint4 *>(to + 8 * i) = act8::load_row8(src + row * cols, c, cols, src + rows * cols);
+}
+
+cudaError_t launch_pad(const uint16_t *src, int64_t rows, int64_t cols, uint16_t *to, cudaStream_t st) {
+    const int64_t chunks = (cols + 7) / 8, ctas = (rows * chunks + 255) / 256;
+    if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    k_pad<<<static_cast<unsigned>(ctas), 256, 0, st>>>(src, rows, cols, chunks, to);
+    count_launch();
+    return cudaGetLastError();
+}
+
 // Clusters of 1 .. 8 CTAs, one on an SM, that are resident at once: of the current context, kept per host thread.
 struct Fits {
     uint64_t ctx = 0;
@@ -1116,20 +1141,42 @@ int pass_chunks(int rp) { return (3 * rp + 63) / 64; }
 
 }  // namespace
 
-size_t act8_grads_tc_workspace_bytes(int64_t M, int r) {
-    return 2 * ((static_cast<size_t>(M) * pass_chunks(pass_rank(r)) * 128 + 255) & ~size_t(255));
-}
+namespace {
 
-bool act8_grads_tc_supported(int64_t M, int64_t n, int r) { return n % 8 == 0 && r % 8 == 0 && M > 0; }
+size_t up256(size_t b) { return (b + 255) & ~size_t(255); }
+size_t mid_bytes(int64_t M, int r) { return up256(static_cast<size_t>(M) * pass_chunks(pass_rank(r)) * 128); }
+int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
+
+}  // namespace
+
+size_t act8_grads_tc_workspace_bytes(int64_t M, int64_t n, int r) {
+    return 2 * mid_bytes(M, r) + (n % 8 ? up256(2 * static_cast<size_t>(M) * static_cast<size_t>(up8(n))) : 0) +
+           (r % 8 ? up256(2 * static_cast<size_t>(n) * static_cast<size_t>(up8(r))) : 0);
+}
 
 cudaError_t launch_act8_grads_tc(const int8_t *codes, const uint16_t *absmax, const uint16_t *gh, int64_t M, int64_t n,
                                  int64_t k, const uint16_t *A, const uint16_t *B, int r, float s,
                                  const DropoutArgs &drop, float *grad_A, float *grad_B, void *ws, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
     TcArgs p{absmax, M, n, k, r, 0, 0, 0, s * (128.0f / 127.0f), grad_A, grad_B, static_cast<uint16_t *>(ws), nullptr, drop};
-    p.u = reinterpret_cast<uint16_t *>(static_cast<char *>(ws) + act8_grads_tc_workspace_bytes(M, r) / 2);
+    char *at = static_cast<char *>(ws) + mid_bytes(M, r);
+    p.u = reinterpret_cast<uint16_t *>(at);
+    at += mid_bytes(M, r);
+    if (n % 8) {
+        uint16_t *to = reinterpret_cast<uint16_t *>(at);
+        at += up256(2 * static_cast<size_t>(M) * static_cast<size_t>(up8(n)));
+        e = launch_pad(gh, M, n, to, st);
+        if (e != cudaSuccess) return e;
+        gh = to;
+    }
+    if (r % 8) {
+        uint16_t *to = reinterpret_cast<uint16_t *>(at);
+        e = launch_pad(B, n, r, to, st);
+        if (e != cudaSuccess) return e;
+        B = to;
+    }
     CUtensorMap tm_gh, tm_codes, tm_A, tm_B, tm_t, tm_u;
-    if (!make_map(&tm_gh, gh, M, n, false) || !make_map(&tm_codes, codes, M, k, true) || !make_map(&tm_B, B, n, r, false))
+    if (!make_map(&tm_gh, gh, M, up8(n), false) || !make_map(&tm_codes, codes, M, k, true) || !make_map(&tm_B, B, n, up8(r), false))
         return cudaErrorInvalidValue;
     const int64_t tok = (M + kDownTile - 1) / kDownTile, tiles = (n + kColsGh - 1) / kColsGh + (k + kColsX - 1) / kColsX;
     if (tok > (int64_t(1) << 28) || tiles > (int64_t(1) << 28)) return cudaErrorInvalidConfiguration;
@@ -1145,15 +1192,10 @@ cudaError_t launch_act8_grads_tc(const int8_t *codes, const uint16_t *absmax, co
         p.chunks = pass_chunks(p.rp);
         if (!make_map(&tm_A, A, r, k, false, static_cast<uint32_t>(p.rp)) || !make_map(&tm_t, p.t, M, 64 * p.chunks, false) || !make_map(&tm_u, p.u, M, 64 * p.chunks, false)) return cudaErrorInvalidValue;
         const dim3 gd(static_cast<unsigned>(tok * rd), 2, 1), go(static_cast<unsigned>(tiles * ro), 1, 1);
-        if (masked) {
-            e = launch_clusters(k_down_tc<true>, gd, kDownThreads, kDownSmem, rd, false, tm_gh, tm_codes, tm_A, tm_B, p, st);
-            if (e == cudaSuccess)
-                e = launch_clusters(k_outer_tc<true>, go, kOutThreads, kOutSmem, ro, true, tm_gh, tm_codes, tm_t, tm_u, p, st);
-        } else {
-            e = launch_clusters(k_down_tc<false>, gd, kDownThreads, kDownSmem, rd, false, tm_gh, tm_codes, tm_A, tm_B, p, st);
-            if (e == cudaSuccess)
-                e = launch_clusters(k_outer_tc<false>, go, kOutThreads, kOutSmem, ro, true, tm_gh, tm_codes, tm_t, tm_u, p, st);
-        }
+        const auto down = masked ? (p.rp > 32 ? k_down_tc<true, 4> : k_down_tc<true, 2>) : (p.rp > 32 ? k_down_tc<false, 4> : k_down_tc<false, 2>);
+        const auto outer = masked ? k_outer_tc<true> : k_outer_tc<false>;
+        e = launch_clusters(down, gd, kDownThreads, kDownSmem, rd, false, tm_gh, tm_codes, tm_A, tm_B, p, st);
+        if (e == cudaSuccess) e = launch_clusters(outer, go, kOutThreads, kOutSmem, ro, true, tm_gh, tm_codes, tm_t, tm_u, p, st);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

@@ -607,11 +607,12 @@ qn_status swiglu_act8_bwd(const qn_act8 *gate8, const qn_act8 *up8, const void *
                        "swiglu_act8_bwd");
 }
 
-qn_status qlora_lora_grads_act8_workspace_size(int64_t M, int r, size_t *ws_bytes) {
+qn_status qlora_lora_grads_act8_workspace_size(int64_t M, int64_t n_out, int r, size_t *ws_bytes) {
     if (!ws_bytes) return fail(QN_EINVAL, "null output pointer");
     if (M < 0 || M > kMaxDim) return fail(QN_EINVAL, "M=%lld out of range", (long long)M);
+    if (n_out < 0 || n_out > kMaxDim) return fail(QN_EINVAL, "n_out=%lld out of range", (long long)n_out);
     if (r < 1 || r > QN_MAX_RANK) return fail(QN_EINVAL, "rank r=%d outside [1, %d]", r, QN_MAX_RANK);
-    *ws_bytes = act8_grads_workspace_bytes(M, r);
+    *ws_bytes = act8_grads_workspace_bytes(M, n_out, r);
     g_err.clear();
     return QN_OK;
 }
@@ -635,7 +636,7 @@ qn_status qlora_lora_grads_act8(const qn_act8 *x, const void *grad_h, int64_t n_
     if ((reinterpret_cast<uintptr_t>(grad_A) & 3u) != 0 || (reinterpret_cast<uintptr_t>(grad_B) & 3u) != 0)
         return fail(QN_EALIGN, "grad_A or grad_B not 4-byte aligned");
     const bool empty = M == 0 || k == 0 || n_out == 0;
-    const size_t need = act8_grads_workspace_bytes(M, r);
+    const size_t need = act8_grads_workspace_bytes(M, n_out, r);
     if (!empty) {
         if (!A || !B) return fail(QN_EINVAL, "null adapter pointer with r=%d", r);
         if (!grad_h) return fail(QN_EINVAL, "null activation pointer");

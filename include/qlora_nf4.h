@@ -363,9 +363,10 @@ qn_status act8_quantize(const void *x, const qn_act8 *out, void *stream);
 /* act8_dequantize -- x_out[e] = bf16_rn(fl32(q_e * s_b)). Errors: as act8_quantize. */
 qn_status act8_dequantize(const qn_act8 *a, void *x_out, void *stream);
 
-/* Workspace bytes qlora_lora_grads_act8 needs for M tokens and rank r (1..256).
+/* Workspace bytes qlora_lora_grads_act8 needs for M tokens, n_out output features and
+ * rank r (1..256); from 128 tokens on it holds a copy of grad_h where n_out % 8 != 0.
  * Host-only. The workspace's contents on entry do not matter. */
-qn_status qlora_lora_grads_act8_workspace_size(int64_t M, int r, size_t *ws_bytes);
+qn_status qlora_lora_grads_act8_workspace_size(int64_t M, int64_t n_out, int r, size_t *ws_bytes);
 
 /* qlora_lora_grads_act8 -- qlora_lora_grads for an input that was kept in 8 bits: the
  * same gradients, of the values that x reads back (M = x->rows, k_in = x->cols):

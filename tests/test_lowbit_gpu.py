@@ -288,7 +288,7 @@ def test_grads_are_reproducible_and_stay_inside_their_buffers():
     x8, gh, A, B = grad_inputs(M, n, k, r)
     aw, a = guarded(r * k, torch.float32, 7.0)
     bw, b = guarded(n * r, torch.float32, 7.0)
-    need = qb.lora_grads_act8_workspace_size(M, r)
+    need = qb.lora_grads_act8_workspace_size(M, n, r)
     whole = torch.full((need + 512,), 77, dtype=torch.uint8, device=DEV)
     first = qb.qlora_lora_grads_act8(x8, gh, A, B, 26.0, grad_A=a.view(r, k), grad_B=b.view(n, r),
                                      workspace=whole[256:256 + need])

@@ -99,7 +99,7 @@ def test_lora_grads_act8_refusals(lib, qb):
     x = _act8(qb)  # 4 x 128
     gh, A, B, ga, gb, ws = (P(0x400000 + 0x100000 * i) for i in range(6))
     f = lib.qlora_lora_grads_act8
-    size = qb.lora_grads_act8_workspace_size(4, 16)
+    size = qb.lora_grads_act8_workspace_size(4, 96, 16)
     assert size >= 2 * 16 * 16 * 4
 
     def call(x=x, gh=gh, n=96, A=A, B=B, rank=16, alpha=32.0, d=None, ga=ga, gb=gb, ws=ws, size=size):
@@ -125,9 +125,14 @@ def test_lora_grads_act8_refusals(lib, qb):
     assert f(r(qb.CAct8(4, 0, None, None)), None, 0, None, None, 16, 1.0, None, None, None, None, 0, None) == OK
     assert lib.qn_launch_count(0) == before
     v = ctypes.c_size_t()
-    assert lib.qlora_lora_grads_act8_workspace_size(-1, 16, r(v)) == EINVAL
-    assert lib.qlora_lora_grads_act8_workspace_size(4, 300, r(v)) == EINVAL
-    assert lib.qlora_lora_grads_act8_workspace_size(4, 16, None) == EINVAL
+    assert lib.qlora_lora_grads_act8_workspace_size(-1, 96, 16, r(v)) == EINVAL
+    assert lib.qlora_lora_grads_act8_workspace_size(4, -1, 16, r(v)) == EINVAL
+    assert lib.qlora_lora_grads_act8_workspace_size(4, 96, 300, r(v)) == EINVAL
+    assert lib.qlora_lora_grads_act8_workspace_size(4, 96, 16, None) == EINVAL
+    # odd widths of a long batch: a padded copy of grad_h, and of B for odd ranks
+    even, odd = (qb.lora_grads_act8_workspace_size(1000, n, 16) for n in (4096, 4097))
+    assert odd - even >= 2 * 1000 * 4104
+    assert qb.lora_grads_act8_workspace_size(1000, 4096, 13) - even >= 2 * 4096 * 16
 
 
 def test_int4_sizes(lib, qb):
