@@ -717,6 +717,8 @@ qn_status int4_linear_fwd(const qn_int4_weight *w, const void *x, int64_t M, voi
     if (s != QN_OK) return s;
     if (M < 0) return fail(QN_EINVAL, "M=%lld out of range", (long long)M);
     if (M > kDecodeMaxM) return fail(QN_ESHAPE, "M=%lld is above %d tokens", (long long)M, kDecodeMaxM);
+    if (w->k_in > kInt4LinearMaxK)
+        return fail(QN_ESHAPE, "k_in=%lld is above %lld", (long long)w->k_in, (long long)kInt4LinearMaxK);
     if (M == 0 || w->n_out == 0) return QN_OK;
     if (!h) return fail(QN_EINVAL, "null output pointer");
     if (!aligned16(h)) return fail(QN_EALIGN, "output not 16-byte aligned");
@@ -732,13 +734,9 @@ qn_status int4_linear_fwd(const qn_int4_weight *w, const void *x, int64_t M, voi
                        {w->scale, 2 * gr, false},
                        {w->zero_point, gr, false}};
     if (overlap(sp)) return fail(QN_EINVAL, "h overlaps another buffer");
-    for (int64_t m0 = 0; m0 < M; m0 += kInt4Tokens) {
-        const int mc = static_cast<int>(M - m0 < kInt4Tokens ? M - m0 : kInt4Tokens);
-        cudaError_t e = launch_int4_linear(view(w), static_cast<const uint16_t *>(x) + m0 * w->k_in, mc,
-                                           static_cast<uint16_t *>(h) + m0 * w->n_out, st);
-        if (e != cudaSuccess) return cuda_status(e, "int4_linear_fwd");
-    }
-    return cuda_status(cudaSuccess, "");
+    return cuda_status(launch_int4_linear(view(w), static_cast<const uint16_t *>(x), static_cast<int>(M),
+                                          static_cast<uint16_t *>(h), st),
+                       "int4_linear_fwd");
 }
 
 }  // extern "C"

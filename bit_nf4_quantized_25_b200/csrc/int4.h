@@ -20,8 +20,9 @@ struct Int4View {
 cudaError_t launch_int4_quantize(const uint16_t *W, const Int4View &w, cudaStream_t st);
 cudaError_t launch_int4_dequantize(const Int4View &w, uint16_t *out, cudaStream_t st);
 
-// h = dequant(W) x for M <= kInt4Tokens tokens.
+// h = dequant(W) x, kInt4Tokens tokens (8 for very large k) per launch, k <= kInt4LinearMaxK.
 constexpr int kInt4Tokens = 16;
+constexpr int64_t kInt4LinearMaxK = 65536;
 cudaError_t launch_int4_linear(const Int4View &w, const uint16_t *x, int M, uint16_t *h, cudaStream_t st);
 
 }  // namespace qn

@@ -452,12 +452,14 @@ qn_status int4_dequantize(const qn_int4_weight *w, void *W_out, void *stream);
 
 /* int4_linear_fwd -- h = dequant(W) x for a few tokens (decoding):
  *   h[m, i] = bf16_rn(sum over the groups of row i of s * sum_k (q - z) x[m, k])
- *   x : M x k_in bf16, h : M x n_out bf16 (written, must not overlap x), M <= 64.
- * q - z enters exactly, the sums are fp32. Tokens are taken 16 per launch. For more
- * tokens than 64 the weight is better expanded once (int4_dequantize) for a matrix
- * product.
- * Errors: QN_EINVAL, QN_ESHAPE (shape, M > 64), QN_EALIGN (x, h or codes not 16-byte
- * aligned, scale not 2-byte aligned), QN_ECUDA. */
+ *   x : M x k_in bf16, h : M x n_out bf16 (written, must not overlap another buffer),
+ *   M <= 64, k_in <= 65536 (shared memory holds x).
+ * q - z enters exactly, the sums are fp32; a token's result does not depend on the
+ * other tokens of the call. Tokens are taken 16 per launch (8 when k_in > 32768). For
+ * more tokens than 64 the weight is better expanded once (int4_dequantize) for a
+ * matrix product.
+ * Errors: QN_EINVAL, QN_ESHAPE (shape, M or k_in above these), QN_EALIGN (x, h or codes
+ * not 16-byte aligned, scale not 2-byte aligned), QN_ECUDA. */
 qn_status int4_linear_fwd(const qn_int4_weight *w, const void *x, int64_t M, void *h, void *stream);
 
 /* Static description of a status code. */

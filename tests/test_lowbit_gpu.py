@@ -423,8 +423,8 @@ def check_linear(w, x):
     W = ref.int4_values(w.codes, w.scale, w.zero_point, w.group)
     want, size = x.double() @ W.t(), x.double().abs() @ W.abs().t()
     # products are exact; a group's sum is 8 accumulations of the tensor core (2^-22 of the sum of sizes each at
-    # most), the groups' sums are joined by at most 36 fp32 additions in a row per warp and 8 over the warps
-    # (2^-24 each), and a term may be up to 16/7 of |s (q - z) x| before the subtraction cancels: below 2^-17
+    # most), the groups' sums are joined by at most 48 fp32 additions in a row per warp and 19 over the parts of k
+    # (2^-24 each): below 2^-17
     within(h, want, want.abs() * ref.HALF_STEP + size * 2.0 ** -17 + TINY)
     return h
 
@@ -447,6 +447,11 @@ def test_int4_linear_fewer_groups_than_warps(k, group):
     check_linear(random_int4(40, k, group, True, seed=1), rand(2, k, seed=2))
 
 
+@pytest.mark.parametrize("n,k,M", [(80000, 256, 2), (7700, 24576, 3), (7700, 24576, 16), (48, 36864, 12), (16, 65536, 17)])
+def test_int4_linear_many_rounds_and_long_rows(n, k, M):
+    check_linear(random_int4(n, k, 64, True, seed=n), rand(M, k, seed=k))
+
+
 def test_int4_linear_outliers_and_non_finite_tokens():
     w = random_int4(64, 512, 128, True, seed=1)
     x = rand(4, 512, seed=2)
@@ -465,6 +470,15 @@ def test_int4_linear_tokens_do_not_depend_on_their_neighbours():
     for m in (1, 5, 8, 11):
         assert torch.equal(qb.int4_linear_fwd(w, x[:m]), h[:m])
     assert torch.equal(qb.int4_linear_fwd(w, x), h)
+
+
+@pytest.mark.parametrize("n,k,group", [(4096, 4096, 128), (688, 11008, 32), (64, 36864, 64)])
+def test_int4_linear_token_alone_or_in_a_batch(n, k, group):
+    w = random_int4(n, k, group, True, seed=n)
+    x = rand(33, k, seed=3)
+    h = qb.int4_linear_fwd(w, x)
+    for a, b in ((0, 1), (7, 9), (20, 33)):
+        assert torch.equal(qb.int4_linear_fwd(w, x[a:b]), h[a:b])
 
 
 def test_int4_empty():

@@ -165,6 +165,7 @@ def test_int4_refusals(lib, qb):
     assert f(None, x, 1, h, None) == EINVAL
     assert f(r(w), x, -1, h, None) == EINVAL
     assert f(r(w), x, 65, h, None) == ESHAPE
+    assert f(r(_int4(qb, k=65600)), x, 1, h, None) == ESHAPE
     assert f(r(w), None, 1, h, None) == EINVAL
     assert f(r(w), x, 1, None, None) == EINVAL
     assert f(r(w), P(0x500002), 1, h, None) == EALIGN
