@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 import threading
 
@@ -24,8 +25,9 @@ CONST_DQ, CONST_F32 = 0, 1           # QN_CONST_DQ, QN_CONST_F32
 EXPORTED = ("qn_nf4_sizes", "qn_weight_sizes", "qn_quantize_workspace_size", "nf4_quantize", "nf4_quantize_static_ws", "nf4_dequantize",
             "qlora_workspace_size", "qlora_workspace_check", "qlora_linear_fwd", "qlora_linear_bwd_x",
             "qlora_merge_bf16", "qlora_lora_grads_workspace_size", "qlora_lora_grads", "qlora_linear_fwd_dropout",
-            "qlora_linear_bwd_x_dropout", "qlora_lora_grads_dropout", "qn_act8_sizes", "act8_quantize", "act8_dequantize",
-            "qlora_lora_grads_act8_workspace_size", "qlora_lora_grads_act8", "swiglu_act8_fwd", "swiglu_act8_bwd", "qn_int4_sizes", "int4_quantize", "int4_dequantize", "int4_linear_fwd",
+            "qlora_linear_bwd_x_dropout", "qlora_lora_grads_dropout", "qn_act8_sizes", "act8_quantize",
+            "act8_dequantize", "qlora_lora_grads_act8_workspace_size", "qlora_lora_grads_act8", "swiglu_act8_fwd",
+            "swiglu_act8_bwd", "qn_int4_sizes", "int4_quantize", "int4_dequantize", "int4_linear_fwd",
             "qn_status_string",
             "qn_last_error", "qn_launch_count", "qn_selftest_wait_timeout")
 
@@ -117,8 +119,9 @@ def load(path: str | None = None):
         lib.int4_quantize.argtypes = [P, I4, P]
         lib.int4_dequantize.argtypes = [I4, P, P]
         lib.int4_linear_fwd.argtypes = [I4, P, i64, P, P]
-        for f in ("qlora_lora_grads_act8_workspace_size", "qlora_lora_grads_act8", "qn_act8_sizes", "act8_quantize", "act8_dequantize", "swiglu_act8_fwd", "swiglu_act8_bwd",
-                  "qn_int4_sizes", "int4_quantize", "int4_dequantize", "int4_linear_fwd"):
+        for f in ("qlora_lora_grads_act8_workspace_size", "qlora_lora_grads_act8", "qn_act8_sizes", "act8_quantize",
+                  "act8_dequantize", "swiglu_act8_fwd", "swiglu_act8_bwd", "qn_int4_sizes", "int4_quantize",
+                  "int4_dequantize", "int4_linear_fwd"):
             getattr(lib, f).restype = st
         for f in ("qlora_merge_bf16", "qlora_lora_grads_workspace_size", "qlora_lora_grads", "qn_nf4_sizes", "qn_quantize_workspace_size", "nf4_quantize", "nf4_quantize_static_ws", "nf4_dequantize",
                   "qlora_workspace_size", "qlora_workspace_check", "qlora_linear_fwd", "qlora_linear_bwd_x",
@@ -467,13 +470,13 @@ def qlora_lora_grads(x: torch.Tensor, grad_h: torch.Tensor, A: torch.Tensor, B: 
 
 # ------------------------------------------------------- activations kept in 8 bits
 # The calls below run on the tensors' device, which has to be the current one, on the current (or the
-# given) stream of it.
+# given) stream of it. What they allocate belongs to that stream.
 
 def _stream_here(dev: torch.device, stream=None) -> int:
     """The stream's handle, after checking that `dev` is the device that the library would launch on."""
     if dev.type != "cuda":
         raise ValueError(f"the tensors are on {dev}, not on a CUDA device")
-    here = torch.cuda.current_device()
+    here = torch._C._cuda_getDevice()
     if dev.index != here:
         raise ValueError(f"the tensors are on {dev}, the current device is cuda:{here}")
     if stream is None:
@@ -490,6 +493,15 @@ def _expect(t: torch.Tensor, name: str, dtype: torch.dtype, shape, dev: torch.de
                          f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
 
 
+def _new(stream, make, *args, **kw):
+    """make(...) in the allocations of the stream that the call runs on: memory that another stream has freed may
+    still be in use there, and a workspace dropped at return must not go to another stream before the kernels end."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
 def _matrix(t: torch.Tensor, name: str):
     if t.dim() != 2 or t.dtype != torch.bfloat16:
         raise ValueError(f"{name} must be a 2-D bf16 tensor, got {t.dtype} of shape {tuple(t.shape)}")
@@ -498,6 +510,7 @@ def _matrix(t: torch.Tensor, name: str):
     return t.shape
 
 
+@functools.lru_cache(maxsize=1024)  # asked for with every new buffer
 def act8_sizes(rows: int, cols: int):
     """(codes, absmax) byte sizes of an activation in 8 bits."""
     a, b = ctypes.c_size_t(), ctypes.c_size_t()
@@ -534,7 +547,7 @@ def act8_quantize(x: torch.Tensor, out: Act8 | None = None, stream=None) -> Act8
     M, k = _matrix(x, "x")
     s = _stream_here(x.device, stream)
     if out is None:
-        out = Act8.empty(M, k, x.device)
+        out = _new(stream, Act8.empty, M, k, x.device)
     elif (out.rows, out.cols) != (M, k):
         raise ValueError(f"out holds {out.rows} x {out.cols} values, x is {M} x {k}")
     _check(load().act8_quantize(x.data_ptr(), ctypes.byref(out.c_struct(x.device, "out")), s), "act8_quantize")
@@ -546,13 +559,14 @@ def act8_dequantize(a: Act8, out: torch.Tensor | None = None, stream=None) -> to
     dev = a.codes.device
     s = _stream_here(dev, stream)
     if out is None:
-        out = torch.empty(a.rows, a.cols, dtype=torch.bfloat16, device=dev)
+        out = _new(stream, torch.empty, a.rows, a.cols, dtype=torch.bfloat16, device=dev)
     else:
         _expect(out, "out", torch.bfloat16, (a.rows, a.cols), dev)
     _check(load().act8_dequantize(ctypes.byref(a.c_struct(dev, "a")), out.data_ptr(), s), "act8_dequantize")
     return out
 
 
+@functools.lru_cache(maxsize=1024)
 def lora_grads_act8_workspace_size(M: int, n_out: int, r: int) -> int:
     v = ctypes.c_size_t()
     _check(load().qlora_lora_grads_act8_workspace_size(M, n_out, r, ctypes.byref(v)),
@@ -576,15 +590,15 @@ def qlora_lora_grads_act8(x: Act8, grad_h: torch.Tensor, A: torch.Tensor, B: tor
     _expect(B, "B", bf, (n, r), dev)
     cx = x.c_struct(dev, "x")
     if grad_A is None:
-        grad_A = torch.empty(r, k, dtype=f32, device=dev)
+        grad_A = _new(stream, torch.empty, r, k, dtype=f32, device=dev)
     else:
         _expect(grad_A, "grad_A", f32, (r, k), dev)
     if grad_B is None:
-        grad_B = torch.empty(n, r, dtype=f32, device=dev)
+        grad_B = _new(stream, torch.empty, n, r, dtype=f32, device=dev)
     else:
         _expect(grad_B, "grad_B", f32, (n, r), dev)
     if workspace is None:
-        workspace = torch.empty(lora_grads_act8_workspace_size(M, n, r), dtype=torch.uint8, device=dev)
+        workspace = _new(stream, torch.empty, lora_grads_act8_workspace_size(M, n, r), dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
     d = None if dropout is None else ctypes.byref(_dropout_struct(dropout))
@@ -601,13 +615,13 @@ def swiglu_act8_fwd(gate: torch.Tensor, up: torch.Tensor, out: torch.Tensor | No
     dev = gate.device
     s = _stream_here(dev, stream)
     _expect(up, "up", torch.bfloat16, (M, n), dev)
-    gate8 = Act8.empty(M, n, dev) if gate8 is None else gate8
-    up8 = Act8.empty(M, n, dev) if up8 is None else up8
+    gate8 = _new(stream, Act8.empty, M, n, dev) if gate8 is None else gate8
+    up8 = _new(stream, Act8.empty, M, n, dev) if up8 is None else up8
     for a, nm in ((gate8, "gate8"), (up8, "up8")):
         if (a.rows, a.cols) != (M, n):
             raise ValueError(f"{nm} holds {a.rows} x {a.cols} values, gate is {M} x {n}")
     if out is None:
-        out = torch.empty_like(gate)
+        out = _new(stream, torch.empty_like, gate)
     else:
         _expect(out, "out", torch.bfloat16, (M, n), dev)
     _check(load().swiglu_act8_fwd(gate.data_ptr(), up.data_ptr(), out.data_ptr(),
@@ -627,7 +641,7 @@ def swiglu_act8_bwd(gate8: Act8, up8: Act8, grad_y: torch.Tensor, grad_gate: tor
     if (up8.rows, up8.cols) != (M, n):
         raise ValueError(f"up8 holds {up8.rows} x {up8.cols} values, gate8 {M} x {n}")
     if y8 is None:
-        y8 = Act8.empty(M, n, dev) if recompute else None
+        y8 = _new(stream, Act8.empty, M, n, dev) if recompute else None
     elif not recompute:
         raise ValueError("y8 is given with recompute=False")
     elif (y8.rows, y8.cols) != (M, n):
@@ -635,7 +649,7 @@ def swiglu_act8_bwd(gate8: Act8, up8: Act8, grad_y: torch.Tensor, grad_gate: tor
     grads = []
     for t, nm in ((grad_gate, "grad_gate"), (grad_up, "grad_up")):
         if t is None:
-            t = torch.empty_like(grad_y)
+            t = _new(stream, torch.empty_like, grad_y)
         else:
             _expect(t, nm, torch.bfloat16, (M, n), dev)
         grads.append(t)
@@ -647,6 +661,7 @@ def swiglu_act8_bwd(gate8: Act8, up8: Act8, grad_y: torch.Tensor, grad_gate: tor
 
 # ------------------------------------------- 4-bit integer weights with group scales
 
+@functools.lru_cache(maxsize=1024)
 def int4_sizes(n_out: int, k_in: int, group: int):
     """(codes, scale, zero_point) byte sizes of a weight in 4-bit integers."""
     v = [ctypes.c_size_t() for _ in range(3)]
@@ -695,7 +710,7 @@ def int4_quantize(W: torch.Tensor, out: Int4Weight | None = None, group: int = 1
     n, k = _matrix(W, "W")
     s = _stream_here(W.device, stream)
     if out is None:
-        out = Int4Weight.empty(n, k, group, zero_point, W.device)
+        out = _new(stream, Int4Weight.empty, n, k, group, zero_point, W.device)
     elif (out.n_out, out.k_in) != (n, k):
         raise ValueError(f"out holds a {out.n_out} x {out.k_in} weight, W is {n} x {k}")
     _check(load().int4_quantize(W.data_ptr(), ctypes.byref(out.c_struct(W.device)), s), "int4_quantize")
@@ -706,7 +721,7 @@ def int4_dequantize(w: Int4Weight, out: torch.Tensor | None = None, stream=None)
     dev = w.codes.device
     s = _stream_here(dev, stream)
     if out is None:
-        out = torch.empty(w.n_out, w.k_in, dtype=torch.bfloat16, device=dev)
+        out = _new(stream, torch.empty, w.n_out, w.k_in, dtype=torch.bfloat16, device=dev)
     else:
         _expect(out, "out", torch.bfloat16, (w.n_out, w.k_in), dev)
     _check(load().int4_dequantize(ctypes.byref(w.c_struct(dev)), out.data_ptr(), s), "int4_dequantize")
@@ -721,7 +736,7 @@ def int4_linear_fwd(w: Int4Weight, x: torch.Tensor, out: torch.Tensor | None = N
     if x.shape[1] != w.k_in:
         raise ValueError(f"x has shape {tuple(x.shape)}, the weight takes {w.k_in} features")
     if out is None:
-        out = torch.empty(M, w.n_out, dtype=torch.bfloat16, device=dev)
+        out = _new(stream, torch.empty, M, w.n_out, dtype=torch.bfloat16, device=dev)
     else:
         _expect(out, "out", torch.bfloat16, (M, w.n_out), dev)
     st = load().int4_linear_fwd(ctypes.byref(w.c_struct(dev)), x.data_ptr(), M, out.data_ptr(), s)

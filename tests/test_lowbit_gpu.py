@@ -524,6 +524,23 @@ def test_calls_on_another_stream_and_in_a_graph():
         assert all(torch.equal(a, b) for a, b in zip(kept, step()))
 
 
+def test_results_do_not_land_in_memory_that_the_current_stream_still_uses():
+    x, w = rand(64, 640, seed=1), random_int4(64, 640, 64, True, seed=2)
+    want_a, want_h = qb.act8_quantize(x).codes, qb.int4_linear_fwd(w, x)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for call, want in ((lambda: qb.act8_quantize(x, stream=side).codes, want_a),
+                       (lambda: qb.int4_linear_fwd(w, x, stream=side), want_h)):
+        late = [torch.empty_like(want) for _ in range(4)]
+        torch.cuda._sleep(20_000_000)
+        for t in late:
+            t.zero_()
+        del late, t
+        got = call()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+
+
 def test_binding_refusals_on_the_gpu():
     x = rand(4, 128)
     a = qb.act8_quantize(x)
