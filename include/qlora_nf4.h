@@ -377,6 +377,8 @@ qn_status qlora_lora_grads_act8_workspace_size(int64_t M, int64_t n_out, int r, 
  * operands enter exactly, t and u with 24 bits, all sums are fp32 in a fixed order:
  * results are bit-reproducible. A token whose t or u is not finite makes every
  * gradient that it enters NaN. M, n_out or k_in 0: the gradients are zero.
+ * The kernels' waits are bounded: a call that gives one up leaves NaN in what it could
+ * not compute.
  * ws: at least qlora_lora_grads_act8_workspace_size() bytes, 256-byte aligned.
  * Errors: QN_EINVAL (null pointer, r outside 1..256, alpha not finite, a dropout rate
  * outside [0, 1), an output that overlaps another buffer), QN_ESHAPE, QN_EALIGN (A, B,

@@ -192,6 +192,15 @@ def test_swiglu_gradient_against_differences():
     within(gu, du, du.abs() * 2.0 ** -7 + slack + 1e-6)
 
 
+def test_swiglu_of_one_tensor_as_gate_and_up():
+    x, dy = rand(5, 192, seed=1), rand(5, 192, seed=2)
+    y, g8, u8 = qb.swiglu_act8_fwd(x, x)
+    assert torch.equal(y, qb.swiglu_act8_fwd(x, x.clone())[0]) and torch.equal(g8.codes, u8.codes)
+    got = qb.swiglu_act8_bwd(g8, g8, dy)
+    want = qb.swiglu_act8_bwd(g8, u8, dy)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(got[2].codes, want[2].codes)
+
+
 def test_swiglu_nan_block_reaches_the_gradients():
     gate, up, dy = rand(2, 128, seed=1), rand(2, 128, seed=2), rand(2, 128, seed=3)
     gate[1, 70] = float("inf")
@@ -463,6 +472,17 @@ def test_int4_linear_outliers_and_non_finite_tokens():
     assert bool(h[3].isnan().all()) and not bool(h[:3].isnan().any())
 
 
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_int4_linear_infinite_activations(group):
+    w = random_int4(64, 512, group, True, seed=1)
+    x = rand(3, 512, seed=2)
+    x[0, 17], x[2, 511] = float("inf"), float("-inf")
+    h = qb.int4_linear_fwd(w, x).double()
+    want = x.double() @ ref.int4_values(w.codes, w.scale, w.zero_point, group).t()
+    assert torch.equal(h.isnan(), want.isnan()) and torch.equal(h.isinf(), want.isinf())
+    assert torch.equal(h[h.isinf()], want[want.isinf()])
+
+
 def test_int4_linear_tokens_do_not_depend_on_their_neighbours():
     w = random_int4(300, 1024, 64, True, seed=1)
     x = rand(16, 1024, seed=2)
@@ -522,6 +542,49 @@ def test_calls_on_another_stream_and_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(kept, step()))
+
+
+@pytest.mark.parametrize("M,n,k,r,dropout", [(200, 1001, 448, 70, None), (300, 512, 512, 16, (0.1, 5, 3)), (40, 130, 192, 90, None)])
+def test_grads_in_a_graph(M, n, k, r, dropout):
+    x8, gh, A, B = grad_inputs(M, n, k, r)
+    ws = torch.empty(qb.lora_grads_act8_workspace_size(M, n, r), dtype=torch.uint8, device=DEV)
+    call = lambda: qb.qlora_lora_grads_act8(x8, gh, A, B, 8.0, workspace=ws, dropout=dropout)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = call()
+    for seed in (20, 30):
+        y8, *rest = grad_inputs(M, n, k, r, seed=seed)
+        for t, v in zip((x8.codes, x8.absmax, gh, A, B), (y8.codes, y8.absmax, *rest)):
+            t.copy_(v)
+        graph.replay()
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(kept, call()))
+
+
+def test_calls_side_by_side_on_two_streams():
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    sets = []
+    for i in range(2):
+        x8, gh, A, B = grad_inputs(512, 1024, 1024, 16, seed=10 * i)
+        w = random_int4(4096, 4096, 64, True, seed=i)
+        sets.append((x8, gh, A, B, w, rand(16, 4096, seed=i), rand(64, 1024, seed=i), rand(64, 1024, seed=i + 5)))
+
+    def run(x8, gh, A, B, w, x, gate, up):
+        y, g8, u8 = qb.swiglu_act8_fwd(gate, up)
+        return (*qb.qlora_lora_grads_act8(x8, gh, A, B, 8.0), qb.int4_linear_fwd(w, x), y, qb.swiglu_act8_bwd(g8, u8, up)[0])
+
+    want = [run(*s) for s in sets]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, side in enumerate(sides):
+            with torch.cuda.stream(side):
+                got[i].append(run(*sets[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for g in got[i] for a, b in zip(g, want[i]))
 
 
 def test_results_do_not_land_in_memory_that_the_current_stream_still_uses():
