@@ -42,6 +42,7 @@ struct TcArgs {
     int r, j0;       // this pass: adapter columns j0 .. j0 + rp of r
     int rp;          // 16, 32, 48 or 64
     int chunks;      // 64-column pieces of a row of t or u: its three terms, rp columns each
+    int64_t tile0;   // first column tile of the launch (second kernel)
     float s;         // already times 128 / 127
     float *grad_A, *grad_B;
     uint16_t *t, *u;  // M x 64 chunks
@@ -707,6 +708,7 @@ __device__ __forceinline__ void outer_tc(const CUtensorMap *act, const CUtensorM
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *slot;
+    grid_dependents_launch();
 
     // Warps drain 32 lanes (columns) of an accumulator each: of grad_h's two, warps 2 .. 17 every other 16 of the columns j;
     // of x's, the last four warps all of them. (Were x's drained by its converters, the MMAs would wait for a conversion.)
@@ -756,7 +758,7 @@ __device__ __forceinline__ void outer_tc(const CUtensorMap *act, const CUtensorM
 
     if (warp == 0) {
         if (lane == 0) {
-            // Up to the dependency wait only x and grad_h are read, which the preceding kernel reads too.
+            // Up to the dependency wait only x and grad_h are read, which the preceding kernels read too.
             int i = 0, issued = 0;  // steps whose t or u, and whose activation, is on its way
             Ring mi, ai;
             auto load_act = [&]() {
@@ -1022,7 +1024,7 @@ k_outer_tc(const __grid_constant__ CUtensorMap tm_gh, const __grid_constant__ CU
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kOutRoom + kOutAbsmax);
     const uint32_t rank = cta_rank(), ranks = cta_ranks();
-    const int64_t tile = blockIdx.x / ranks, tiles_gh = (p.n + kColsGh - 1) / kColsGh;
+    const int64_t tile = p.tile0 + blockIdx.x / ranks, tiles_gh = (p.n + kColsGh - 1) / kColsGh;
     if (tile < tiles_gh)
         outer_tc<false, false>(&tm_gh, &tm_t, p, smem, bars, tile, rank, ranks);
     else
@@ -1136,6 +1138,35 @@ int cluster_size(const Fits &fits, int per_sm, int64_t tiles, int64_t steps, int
     return best;
 }
 
+// Column tiles of the second kernel: the first `first` ones in clusters of c CTAs, the rest in clusters of c_rest in a launch of
+// their own, as the least waves x (steps + besides) in all want it (a launch costs `again` more). 112 + 64 tiles of 64 steps
+// (28672 x 8192, 4096 tokens) are three waves of clusters of 2, but one of 148 CTAs and one of 28 clusters.
+struct Split {
+    int64_t first;
+    int c, c_rest;
+};
+
+Split split_tiles(const Fits &fits, int64_t tiles, int64_t steps, int64_t besides, int64_t again) {
+    auto cost = [&](int64_t n, int c) {
+        const int64_t fit = fits.clusters[c];
+        return (n + fit - 1) / fit * ((steps + c - 1) / c + besides);
+    };
+    const int whole = cluster_size(fits, 1, tiles, steps, besides);
+    Split best{tiles, whole, 0};
+    int64_t least = fits.clusters[whole] > 0 ? cost(tiles, whole) : 0;
+    for (int c = 1; c <= 8 && c <= steps; ++c) {
+        const int64_t fit = fits.clusters[c], first = fit > 0 ? tiles / fit * fit : 0;
+        if (first == 0 || first == tiles) continue;
+        const int rest = cluster_size(fits, 1, tiles - first, steps, besides);
+        const int64_t both = cost(first, c) + cost(tiles - first, rest) + again;
+        if (both < least) {
+            least = both;
+            best = {first, c, rest};
+        }
+    }
+    return best;
+}
+
 int pass_rank(int r) { return r >= 64 ? 64 : (r + 15) / 16 * 16; }
 int pass_chunks(int rp) { return (3 * rp + 63) / 64; }
 
@@ -1158,7 +1189,7 @@ cudaError_t launch_act8_grads_tc(const int8_t *codes, const uint16_t *absmax, co
                                  int64_t k, const uint16_t *A, const uint16_t *B, int r, float s,
                                  const DropoutArgs &drop, float *grad_A, float *grad_B, void *ws, cudaStream_t st) {
     cudaError_t e = cudaSuccess;
-    TcArgs p{absmax, M, n, k, r, 0, 0, 0, s * (128.0f / 127.0f), grad_A, grad_B, static_cast<uint16_t *>(ws), nullptr, drop};
+    TcArgs p{absmax, M, n, k, r, 0, 0, 0, 0, s * (128.0f / 127.0f), grad_A, grad_B, static_cast<uint16_t *>(ws), nullptr, drop};
     char *at = static_cast<char *>(ws) + mid_bytes(M, r);
     p.u = reinterpret_cast<uint16_t *>(at);
     at += mid_bytes(M, r);
@@ -1186,16 +1217,26 @@ cudaError_t launch_act8_grads_tc(const int8_t *codes, const uint16_t *absmax, co
     e = cluster_fits(&fits);
     if (e != cudaSuccess) return e;
     // two CTAs of the first kernel share an SM
-    const int rd = cluster_size(*fits, 2, 2 * tok, pieces, 10), ro = cluster_size(*fits, 1, tiles, steps, 12);
+    const int rd = cluster_size(*fits, 2, 2 * tok, pieces, 10);
+    const Split so = split_tiles(*fits, tiles, steps, 12, 4);
     for (p.j0 = 0; p.j0 < r; p.j0 += 64) {
         p.rp = pass_rank(r - p.j0);
         p.chunks = pass_chunks(p.rp);
-        if (!make_map(&tm_A, A, r, k, false, static_cast<uint32_t>(p.rp)) || !make_map(&tm_t, p.t, M, 64 * p.chunks, false) || !make_map(&tm_u, p.u, M, 64 * p.chunks, false)) return cudaErrorInvalidValue;
-        const dim3 gd(static_cast<unsigned>(tok * rd), 2, 1), go(static_cast<unsigned>(tiles * ro), 1, 1);
-        const auto down = masked ? (p.rp > 32 ? k_down_tc<true, 4> : k_down_tc<true, 2>) : (p.rp > 32 ? k_down_tc<false, 4> : k_down_tc<false, 2>);
+        if (!make_map(&tm_A, A, r, k, false, static_cast<uint32_t>(p.rp)) ||
+            !make_map(&tm_t, p.t, M, 64 * p.chunks, false) || !make_map(&tm_u, p.u, M, 64 * p.chunks, false))
+            return cudaErrorInvalidValue;
+        const auto down = masked ? (p.rp > 32 ? k_down_tc<true, 4> : k_down_tc<true, 2>)
+                                 : (p.rp > 32 ? k_down_tc<false, 4> : k_down_tc<false, 2>);
         const auto outer = masked ? k_outer_tc<true> : k_outer_tc<false>;
-        e = launch_clusters(down, gd, kDownThreads, kDownSmem, rd, false, tm_gh, tm_codes, tm_A, tm_B, p, st);
-        if (e == cudaSuccess) e = launch_clusters(outer, go, kOutThreads, kOutSmem, ro, true, tm_gh, tm_codes, tm_t, tm_u, p, st);
+        const auto grid = [](int64_t n, int c, unsigned y) { return dim3(static_cast<unsigned>(n * c), y, 1); };
+        e = launch_clusters(down, grid(tok, rd, 2), kDownThreads, kDownSmem, rd, false, tm_gh, tm_codes, tm_A, tm_B, p, st);
+        p.tile0 = 0;
+        if (e == cudaSuccess)
+            e = launch_clusters(outer, grid(so.first, so.c, 1), kOutThreads, kOutSmem, so.c, true, tm_gh, tm_codes, tm_t, tm_u, p, st);
+        p.tile0 = so.first;
+        if (e == cudaSuccess && so.first < tiles)
+            e = launch_clusters(outer, grid(tiles - so.first, so.c_rest, 1), kOutThreads, kOutSmem, so.c_rest, true, tm_gh, tm_codes,
+                                tm_t, tm_u, p, st);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
