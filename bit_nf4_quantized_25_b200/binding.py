@@ -486,10 +486,10 @@ def _stream_here(dev: torch.device, stream=None) -> int:
     return stream.cuda_stream
 
 
-def _expect(t: torch.Tensor, name: str, dtype: torch.dtype, shape, dev: torch.device):
+def _expect(t: torch.Tensor, name: str, dtype: torch.dtype, shape, dev: torch.device, part: str = ""):
     """t is a contiguous tensor of this type and shape on `dev`: the library sees only its address."""
     if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got "
+        raise ValueError(f"{name}{part} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
 
 
@@ -534,8 +534,11 @@ class Act8:
                     torch.empty(rows, cols // BLOCK, dtype=torch.bfloat16, device=device))
 
     def c_struct(self, dev: torch.device, name: str = "Act8") -> CAct8:
-        _expect(self.codes, f"{name}.codes", torch.int8, (self.rows, self.cols), dev)
-        _expect(self.absmax, f"{name}.absmax", torch.bfloat16, (self.rows, self.cols // BLOCK), dev)
+        _expect(self.codes, name, torch.int8, (self.rows, self.cols), dev, ".codes")
+        _expect(self.absmax, name, torch.bfloat16, (self.rows, self.cols // BLOCK), dev, ".absmax")
+        return self._c()
+
+    def _c(self) -> CAct8:  # of checked buffers, or new ones
         return CAct8(self.rows, self.cols, self.codes.data_ptr(), self.absmax.data_ptr())
 
     def nbytes(self) -> int:
@@ -548,9 +551,14 @@ def act8_quantize(x: torch.Tensor, out: Act8 | None = None, stream=None) -> Act8
     s = _stream_here(x.device, stream)
     if out is None:
         out = _new(stream, Act8.empty, M, k, x.device)
+        c = out._c()
     elif (out.rows, out.cols) != (M, k):
         raise ValueError(f"out holds {out.rows} x {out.cols} values, x is {M} x {k}")
-    _check(load().act8_quantize(x.data_ptr(), ctypes.byref(out.c_struct(x.device, "out")), s), "act8_quantize")
+    else:
+        c = out.c_struct(x.device, "out")
+    st = load().act8_quantize(x.data_ptr(), ctypes.byref(c), s)
+    if st != QN_OK:
+        _check(st, "act8_quantize")
     return out
 
 
@@ -562,7 +570,9 @@ def act8_dequantize(a: Act8, out: torch.Tensor | None = None, stream=None) -> to
         out = _new(stream, torch.empty, a.rows, a.cols, dtype=torch.bfloat16, device=dev)
     else:
         _expect(out, "out", torch.bfloat16, (a.rows, a.cols), dev)
-    _check(load().act8_dequantize(ctypes.byref(a.c_struct(dev, "a")), out.data_ptr(), s), "act8_dequantize")
+    st = load().act8_dequantize(ctypes.byref(a.c_struct(dev, "a")), out.data_ptr(), s)
+    if st != QN_OK:
+        _check(st, "act8_dequantize")
     return out
 
 
@@ -615,19 +625,25 @@ def swiglu_act8_fwd(gate: torch.Tensor, up: torch.Tensor, out: torch.Tensor | No
     dev = gate.device
     s = _stream_here(dev, stream)
     _expect(up, "up", torch.bfloat16, (M, n), dev)
-    gate8 = _new(stream, Act8.empty, M, n, dev) if gate8 is None else gate8
-    up8 = _new(stream, Act8.empty, M, n, dev) if up8 is None else up8
+    kept, structs = [], []
     for a, nm in ((gate8, "gate8"), (up8, "up8")):
-        if (a.rows, a.cols) != (M, n):
+        if a is None:
+            a = _new(stream, Act8.empty, M, n, dev)
+            structs.append(a._c())
+        elif (a.rows, a.cols) != (M, n):
             raise ValueError(f"{nm} holds {a.rows} x {a.cols} values, gate is {M} x {n}")
+        else:
+            structs.append(a.c_struct(dev, nm))
+        kept.append(a)
     if out is None:
         out = _new(stream, torch.empty_like, gate)
     else:
         _expect(out, "out", torch.bfloat16, (M, n), dev)
-    _check(load().swiglu_act8_fwd(gate.data_ptr(), up.data_ptr(), out.data_ptr(),
-                                  ctypes.byref(gate8.c_struct(dev, "gate8")), ctypes.byref(up8.c_struct(dev, "up8")), s),
-           "swiglu_act8_fwd")
-    return out, gate8, up8
+    st = load().swiglu_act8_fwd(gate.data_ptr(), up.data_ptr(), out.data_ptr(), ctypes.byref(structs[0]),
+                                ctypes.byref(structs[1]), s)
+    if st != QN_OK:
+        _check(st, "swiglu_act8_fwd")
+    return out, kept[0], kept[1]
 
 
 def swiglu_act8_bwd(gate8: Act8, up8: Act8, grad_y: torch.Tensor, grad_gate: torch.Tensor | None = None,
@@ -640,12 +656,17 @@ def swiglu_act8_bwd(gate8: Act8, up8: Act8, grad_y: torch.Tensor, grad_gate: tor
     _expect(grad_y, "grad_y", torch.bfloat16, (M, n), dev)
     if (up8.rows, up8.cols) != (M, n):
         raise ValueError(f"up8 holds {up8.rows} x {up8.cols} values, gate8 {M} x {n}")
+    cy = None
     if y8 is None:
-        y8 = _new(stream, Act8.empty, M, n, dev) if recompute else None
+        if recompute:
+            y8 = _new(stream, Act8.empty, M, n, dev)
+            cy = ctypes.byref(y8._c())
     elif not recompute:
         raise ValueError("y8 is given with recompute=False")
     elif (y8.rows, y8.cols) != (M, n):
         raise ValueError(f"y8 holds {y8.rows} x {y8.cols} values, gate8 {M} x {n}")
+    else:
+        cy = ctypes.byref(y8.c_struct(dev, "y8"))
     grads = []
     for t, nm in ((grad_gate, "grad_gate"), (grad_up, "grad_up")):
         if t is None:
@@ -653,9 +674,10 @@ def swiglu_act8_bwd(gate8: Act8, up8: Act8, grad_y: torch.Tensor, grad_gate: tor
         else:
             _expect(t, nm, torch.bfloat16, (M, n), dev)
         grads.append(t)
-    _check(load().swiglu_act8_bwd(ctypes.byref(gate8.c_struct(dev, "gate8")), ctypes.byref(up8.c_struct(dev, "up8")),
-                                  grad_y.data_ptr(), grads[0].data_ptr(), grads[1].data_ptr(),
-                                  None if y8 is None else ctypes.byref(y8.c_struct(dev, "y8")), s), "swiglu_act8_bwd")
+    st = load().swiglu_act8_bwd(ctypes.byref(gate8.c_struct(dev, "gate8")), ctypes.byref(up8.c_struct(dev, "up8")),
+                                grad_y.data_ptr(), grads[0].data_ptr(), grads[1].data_ptr(), cy, s)
+    if st != QN_OK:
+        _check(st, "swiglu_act8_bwd")
     return grads[0], grads[1], y8
 
 
@@ -693,9 +715,12 @@ class Int4Weight:
         groups = (self.n_out, self.k_in // self.group)
         _expect(self.codes, "codes", torch.uint8, (self.n_out, self.k_in // 2), dev)
         _expect(self.scale, "scale", torch.bfloat16, groups, dev)
+        if self.zero_point is not None:
+            _expect(self.zero_point, "zero_point", torch.uint8, groups, dev)
+        return self._c()
+
+    def _c(self) -> CInt4:  # of checked buffers, or new ones
         z = self.zero_point
-        if z is not None:
-            _expect(z, "zero_point", torch.uint8, groups, dev)
         return CInt4(self.n_out, self.k_in, self.group, self.codes.data_ptr(), self.scale.data_ptr(),
                      None if z is None else z.data_ptr())
 
@@ -711,9 +736,14 @@ def int4_quantize(W: torch.Tensor, out: Int4Weight | None = None, group: int = 1
     s = _stream_here(W.device, stream)
     if out is None:
         out = _new(stream, Int4Weight.empty, n, k, group, zero_point, W.device)
+        c = out._c()
     elif (out.n_out, out.k_in) != (n, k):
         raise ValueError(f"out holds a {out.n_out} x {out.k_in} weight, W is {n} x {k}")
-    _check(load().int4_quantize(W.data_ptr(), ctypes.byref(out.c_struct(W.device)), s), "int4_quantize")
+    else:
+        c = out.c_struct(W.device)
+    st = load().int4_quantize(W.data_ptr(), ctypes.byref(c), s)
+    if st != QN_OK:
+        _check(st, "int4_quantize")
     return out
 
 
