@@ -16,6 +16,7 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libqlora_nf4.so")
+MARSHAL_PATH = os.path.join(_PKG, "_marshal.so")
 
 QN_OK, QN_EINVAL, QN_ESHAPE, QN_EALIGN, QN_ECUDA, QN_EWORKSPACE, QN_ETIMEOUT = range(7)
 BLOCK, GROUP, MAX_RANK = 64, 256, 256
@@ -472,6 +473,25 @@ def qlora_lora_grads(x: torch.Tensor, grad_h: torch.Tensor, A: torch.Tensor, B: 
 # The calls below run on the tensors' device, which has to be the current one, on the current (or the
 # given) stream of it. What they allocate belongs to that stream.
 
+_marshal = None
+
+
+def _native():
+    """The compiled marshalling of the plain calls (csrc/marshal.cpp): new results, current stream. A call of it gives the
+    results, a status, or None when the operands need the general way below."""
+    global _marshal
+    if _marshal is None:
+        lib = load()
+        if not os.path.exists(MARSHAL_PATH):
+            raise RuntimeError(f"{MARSHAL_PATH} is missing: build it with `python -m bit_nf4_quantized_25_b200.build`")
+        from . import _marshal as m
+        m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.act8_quantize, lib.act8_dequantize, lib.qlora_lora_grads_act8_workspace_size, lib.qlora_lora_grads_act8,
+            lib.swiglu_act8_fwd, lib.swiglu_act8_bwd, lib.int4_quantize, lib.int4_dequantize, lib.int4_linear_fwd)))
+        _marshal = m
+    return _marshal
+
+
 def _stream_here(dev: torch.device, stream=None) -> int:
     """The stream's handle, after checking that `dev` is the device that the library would launch on."""
     if dev.type != "cuda":
@@ -491,6 +511,13 @@ def _expect(t: torch.Tensor, name: str, dtype: torch.dtype, shape, dev: torch.de
     if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
         raise ValueError(f"{name}{part} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+
+
+def _done(r, what: str):
+    """What a native call gave, unless it is a status."""
+    if type(r) is int:
+        _check(r, what)
+    return r
 
 
 def _new(stream, make, *args, **kw):
@@ -547,6 +574,10 @@ class Act8:
 
 def act8_quantize(x: torch.Tensor, out: Act8 | None = None, stream=None) -> Act8:
     """An activation (M x k, bf16) in 8 bits, to keep for the backward pass."""
+    if out is None and stream is None:
+        r = _native().act8_quantize(x)
+        if r is not None:
+            return Act8(*x.shape, *_done(r, "act8_quantize"))
     M, k = _matrix(x, "x")
     s = _stream_here(x.device, stream)
     if out is None:
@@ -564,6 +595,10 @@ def act8_quantize(x: torch.Tensor, out: Act8 | None = None, stream=None) -> Act8
 
 def act8_dequantize(a: Act8, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The bf16 values of an activation in 8 bits."""
+    if out is None and stream is None:
+        r = _native().act8_dequantize(a.rows, a.cols, a.codes, a.absmax)
+        if r is not None:
+            return _done(r, "act8_dequantize")
     dev = a.codes.device
     s = _stream_here(dev, stream)
     if out is None:
@@ -589,6 +624,10 @@ def qlora_lora_grads_act8(x: Act8, grad_h: torch.Tensor, A: torch.Tensor, B: tor
                           workspace: torch.Tensor | None = None, stream=None, dropout=None):
     """(grad_A (r x k_in), grad_B (n_out x r)) in fp32 for an input x kept in 8 bits and grad_h (M x n_out).
     dropout = (p, seed, offset): the forward's LoRA-dropout mask."""
+    if grad_A is None and grad_B is None and workspace is None and stream is None and dropout is None:
+        r = _native().lora_grads(x.rows, x.cols, x.codes, x.absmax, grad_h, A, B, float(alpha))
+        if r is not None:
+            return _done(r, "qlora_lora_grads_act8")
     M, k = x.rows, x.cols
     n = _matrix(grad_h, "grad_h")[1]
     r = _matrix(A, "A")[0]
@@ -621,6 +660,12 @@ def qlora_lora_grads_act8(x: Act8, grad_h: torch.Tensor, A: torch.Tensor, B: tor
 def swiglu_act8_fwd(gate: torch.Tensor, up: torch.Tensor, out: torch.Tensor | None = None, gate8: Act8 | None = None,
                     up8: Act8 | None = None, stream=None):
     """(y, gate8, up8): y = silu(gate) * up in bf16, and gate and up in 8 bits for swiglu_act8_bwd."""
+    if out is None and gate8 is None and up8 is None and stream is None:
+        r = _native().swiglu_fwd(gate, up)
+        if r is not None:
+            y, gc, ga, uc, ua = _done(r, "swiglu_act8_fwd")
+            M, n = gate.shape
+            return y, Act8(M, n, gc, ga), Act8(M, n, uc, ua)
     M, n = _matrix(gate, "gate")
     dev = gate.device
     s = _stream_here(dev, stream)
@@ -651,6 +696,11 @@ def swiglu_act8_bwd(gate8: Act8, up8: Act8, grad_y: torch.Tensor, grad_gate: tor
     """(grad_gate, grad_up, y8) from what swiglu_act8_fwd kept; y8 is y once more, in 8 bits, the input that the
     next layer's adapter gradients take (None with recompute=False)."""
     M, n = gate8.rows, gate8.cols
+    if grad_gate is None and grad_up is None and y8 is None and stream is None and recompute:
+        r = _native().swiglu_bwd(M, n, gate8.codes, gate8.absmax, up8.rows, up8.cols, up8.codes, up8.absmax, grad_y)
+        if r is not None:
+            gg, gu, yc, ya = _done(r, "swiglu_act8_bwd")
+            return gg, gu, Act8(M, n, yc, ya)
     dev = gate8.codes.device
     s = _stream_here(dev, stream)
     _expect(grad_y, "grad_y", torch.bfloat16, (M, n), dev)
@@ -732,6 +782,10 @@ def int4_quantize(W: torch.Tensor, out: Int4Weight | None = None, group: int = 1
                   stream=None) -> Int4Weight:
     """Quantise a bf16 (n_out x k_in) weight, a merged one for instance, to 4-bit integers; an `out` given keeps its
     own group and zero points."""
+    if out is None and stream is None:
+        r = _native().int4_quantize(W, group, zero_point)
+        if r is not None:
+            return Int4Weight(*W.shape, group, *_done(r, "int4_quantize"))
     n, k = _matrix(W, "W")
     s = _stream_here(W.device, stream)
     if out is None:
@@ -748,6 +802,11 @@ def int4_quantize(W: torch.Tensor, out: Int4Weight | None = None, group: int = 1
 
 
 def int4_dequantize(w: Int4Weight, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The bf16 weight that w stands for."""
+    if out is None and stream is None:
+        r = _native().int4_dequantize(w.n_out, w.k_in, w.group, w.codes, w.scale, w.zero_point)
+        if r is not None:
+            return _done(r, "int4_dequantize")
     dev = w.codes.device
     s = _stream_here(dev, stream)
     if out is None:
@@ -760,6 +819,10 @@ def int4_dequantize(w: Int4Weight, out: torch.Tensor | None = None, stream=None)
 
 def int4_linear_fwd(w: Int4Weight, x: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """h = dequant(W) x for at most 64 tokens; x is M x k_in, h is M x n_out (bf16)."""
+    if out is None and stream is None:
+        r = _native().int4_linear(w.n_out, w.k_in, w.group, w.codes, w.scale, w.zero_point, x)
+        if r is not None:
+            return _done(r, "int4_linear_fwd")
     dev = x.device
     s = _stream_here(dev, stream)
     M = _matrix(x, "x")[0]

@@ -177,6 +177,25 @@ def test_int4_refusals(lib, qb):
     assert lib.qn_launch_count(0) == before
 
 
+def test_the_compiled_marshalling_leaves_what_is_not_plain_to_the_general_way(lib, qb):
+    m = qb._native()
+    bf = torch.bfloat16
+    x, codes, absmax = torch.zeros(2, 64, dtype=bf), torch.zeros(2, 64, dtype=torch.int8), torch.zeros(2, 1, dtype=bf)
+    u8 = torch.zeros(2, 32, dtype=torch.uint8)
+    for call, operands in ((m.act8_quantize, (x,)), (m.act8_dequantize, (2, 64, codes, absmax)),
+                           (m.lora_grads, (2, 64, codes, absmax, x, x, x, 1.0)), (m.swiglu_fwd, (x, x)),
+                           (m.swiglu_bwd, (2, 64, codes, absmax, 2, 64, codes, absmax, x)), (m.int4_quantize, (x, 64, True)),
+                           (m.int4_dequantize, (2, 64, 64, u8, absmax, None)), (m.int4_linear, (2, 64, 64, u8, absmax, None, x))):
+        assert call(*operands) is None  # not on a GPU
+        assert call(*(None for _ in operands)) is None
+        with pytest.raises(TypeError, match="arguments"):
+            call(*operands, 0)
+    with pytest.raises(TypeError):
+        m.bind(1)
+    with pytest.raises(ValueError, match="null"):
+        m.bind(*[0] * 9)
+
+
 def test_binding_refuses_before_the_library(qb):
     bf = torch.bfloat16
     with pytest.raises(ValueError, match="not on a CUDA device"):
