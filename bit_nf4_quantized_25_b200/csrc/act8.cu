@@ -14,6 +14,7 @@
 // kUnroll words, all loaded before the first is used.
 #include "act8.cuh"
 #include "act8.h"
+#include "dependent.cuh"
 
 namespace qn {
 
@@ -54,6 +55,7 @@ template <int kUnroll>
 __global__ void __launch_bounds__(kThreads) k_act8_quantize(const uint16_t *x, int64_t words, int8_t *codes,
                                                             uint16_t *absmax) {
     const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kThreads * kUnroll) + threadIdx.x;
+    begin_dependent();
     uint4 v[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -71,6 +73,7 @@ template <int kUnroll>
 __global__ void __launch_bounds__(kThreads) k_act8_dequantize(const int8_t *codes, const uint16_t *absmax,
                                                               int64_t words, uint16_t *x) {
     const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kThreads * kUnroll) + threadIdx.x;
+    begin_dependent();
     uint2 q[kUnroll];
     uint32_t top[kUnroll];
 #pragma unroll
@@ -78,7 +81,7 @@ __global__ void __launch_bounds__(kThreads) k_act8_dequantize(const int8_t *code
         const int64_t i = i0 + u * kThreads;
         const bool live = i < words;
         q[u] = live ? ld_nc_v2(codes + act8::kPer * i) : make_uint2(0u, 0u);
-        top[u] = live ? ld_ro_u16(absmax + i / act8::kLanes) : 0u;
+        top[u] = live ? ld_nc_u16(absmax + i / act8::kLanes) : 0u;
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -95,6 +98,7 @@ __global__ void __launch_bounds__(kThreads) k_swiglu_act8_fwd(const uint16_t *ga
                                                               uint16_t *y, int8_t *gq, uint16_t *ga, int8_t *uq,
                                                               uint16_t *ua) {
     const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kThreads * kUnroll) + threadIdx.x;
+    begin_dependent();
     uint4 g[kUnroll], w[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -124,6 +128,7 @@ __global__ void __launch_bounds__(kThreads) k_swiglu_act8_bwd(const int8_t *gq, 
                                                               int64_t words, uint16_t *grad_gate, uint16_t *grad_up,
                                                               int8_t *yq, uint16_t *ya) {
     const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kThreads * kUnroll) + threadIdx.x;
+    begin_dependent();
     uint4 d[kUnroll];
     uint2 g[kUnroll], w[kUnroll];
     uint32_t gt[kUnroll], ut[kUnroll];
@@ -134,8 +139,8 @@ __global__ void __launch_bounds__(kThreads) k_swiglu_act8_bwd(const int8_t *gq, 
         d[u] = live ? ld_nc_v4(grad_y + act8::kPer * i) : make_uint4(0u, 0u, 0u, 0u);
         g[u] = live ? ld_nc_v2(gq + act8::kPer * i) : make_uint2(0u, 0u);
         w[u] = live ? ld_nc_v2(uq + act8::kPer * i) : make_uint2(0u, 0u);
-        gt[u] = live ? ld_ro_u16(ga + i / act8::kLanes) : 0u;
-        ut[u] = live ? ld_ro_u16(ua + i / act8::kLanes) : 0u;
+        gt[u] = live ? ld_nc_u16(ga + i / act8::kLanes) : 0u;
+        ut[u] = live ? ld_nc_u16(ua + i / act8::kLanes) : 0u;
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -172,9 +177,7 @@ cudaError_t launch_act8_quantize(const uint16_t *x, int64_t count, int8_t *codes
     const int64_t words = count / act8::kPer;
     const unsigned grid = grid_for(words, 4);
     if (grid == 0) return cudaErrorInvalidConfiguration;
-    k_act8_quantize<4><<<grid, kThreads, 0, st>>>(x, words, codes, absmax);
-    count_launch();
-    return cudaGetLastError();
+    return launch_dependent(k_act8_quantize<4>, grid, kThreads, st, x, words, codes, absmax);
 }
 
 cudaError_t launch_act8_dequantize(const int8_t *codes, const uint16_t *absmax, int64_t count, uint16_t *x,
@@ -182,9 +185,7 @@ cudaError_t launch_act8_dequantize(const int8_t *codes, const uint16_t *absmax, 
     const int64_t words = count / act8::kPer;
     const unsigned grid = grid_for(words, 4);
     if (grid == 0) return cudaErrorInvalidConfiguration;
-    k_act8_dequantize<4><<<grid, kThreads, 0, st>>>(codes, absmax, words, x);
-    count_launch();
-    return cudaGetLastError();
+    return launch_dependent(k_act8_dequantize<4>, grid, kThreads, st, codes, absmax, words, x);
 }
 
 cudaError_t launch_swiglu_act8_fwd(const uint16_t *gate, const uint16_t *up, int64_t count, uint16_t *y,
@@ -193,9 +194,8 @@ cudaError_t launch_swiglu_act8_fwd(const uint16_t *gate, const uint16_t *up, int
     const int64_t words = count / act8::kPer;
     const unsigned grid = grid_for(words, 2);
     if (grid == 0) return cudaErrorInvalidConfiguration;
-    k_swiglu_act8_fwd<2><<<grid, kThreads, 0, st>>>(gate, up, words, y, gate_codes, gate_absmax, up_codes, up_absmax);
-    count_launch();
-    return cudaGetLastError();
+    return launch_dependent(k_swiglu_act8_fwd<2>, grid, kThreads, st, gate, up, words, y, gate_codes, gate_absmax, up_codes,
+                            up_absmax);
 }
 
 cudaError_t launch_swiglu_act8_bwd(const int8_t *gate_codes, const uint16_t *gate_absmax, const int8_t *up_codes,
@@ -205,10 +205,8 @@ cudaError_t launch_swiglu_act8_bwd(const int8_t *gate_codes, const uint16_t *gat
     const int64_t words = count / act8::kPer;
     const unsigned grid = grid_for(words, 2);
     if (grid == 0) return cudaErrorInvalidConfiguration;
-    k_swiglu_act8_bwd<2><<<grid, kThreads, 0, st>>>(gate_codes, gate_absmax, up_codes, up_absmax, grad_y, words,
-                                                    grad_gate, grad_up, y_codes, y_absmax);
-    count_launch();
-    return cudaGetLastError();
+    return launch_dependent(k_swiglu_act8_bwd<2>, grid, kThreads, st, gate_codes, gate_absmax, up_codes, up_absmax, grad_y, words,
+                            grad_gate, grad_up, y_codes, y_absmax);
 }
 
 }  // namespace qn

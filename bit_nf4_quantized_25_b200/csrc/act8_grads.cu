@@ -291,6 +291,7 @@ __global__ void __launch_bounds__(kDownThreads) k_down(const GradArgs p) {
     extern __shared__ __align__(16) float red[];
     const uint32_t rank = cluster_rank(), ranks = cluster_size();
     const int64_t tile = blockIdx.x / ranks;
+    grid_dependents_launch();
     if (blockIdx.y == 0)
         down<NT, false, false>(p, red, tile, rank, ranks);
     else
@@ -353,6 +354,7 @@ __device__ __forceinline__ void outer(const GradArgs &p, float *red, int64_t til
     int64_t m16 = rank * kTokWarps + tw;
     const bool work = col0 < width;
     if (work && m16 < tiles16) load(m16);
+    grid_dependency_wait();  // for t and u; x and grad_h were there before the first kernel
     for (; work && m16 < tiles16; m16 += step) {
         uint32_t a[4][4];  // [pair of columns 8 g + 2 i, + 1][tokens 0 1 | tokens 0 1 of the next column | 2 3 | 2 3]
         float sc[4];
@@ -473,25 +475,32 @@ __global__ void __launch_bounds__(kOutThreads) k_outer(const GradArgs p) {
 }
 
 template <typename K>
-cudaError_t launch_clusters(K kern, dim3 grid, int threads, size_t smem, int ranks, const GradArgs &p, cudaStream_t st) {
-    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kern), smem);
+cudaError_t launch_clusters(K kern, dim3 grid, int threads, size_t smem, int ranks, bool dependent, const GradArgs &p,
+                            cudaStream_t st) {
+    cudaError_t e = smem > 48 * 1024 ? ensure_smem_limit(reinterpret_cast<const void *>(kern), smem) : cudaSuccess;
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    unsigned n = 0;
+    if (dependent) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (ranks > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = static_cast<unsigned>(ranks);
+        attr[n].val.clusterDim.y = 1;
+        attr[n++].val.clusterDim.z = 1;
+    }
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = n;
     e = cudaLaunchKernelEx(&cfg, kern, p);
-    if (e != cudaSuccess) return e;
-    count_launch();
-    return cudaGetLastError();
+    if (e == cudaSuccess) count_launch();
+    return e;
 }
 
 // CTAs that share a tile: doubled until the grid has `want` CTAs, at most 8 and at most `most`.
@@ -508,13 +517,13 @@ cudaError_t launch_pass(const GradArgs &p, int sms, cudaStream_t st) {
     int ranks = split_ranks(2 * tok, 2 * sms, rounds);
     if (tok * ranks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     cudaError_t e = launch_clusters(k_down<NT, kDrop>, dim3(static_cast<unsigned>(tok * ranks), 2, 1), kDownThreads,
-                                    static_cast<size_t>(kDownWarps) * kDownTokens * (8 * NT + 1) * 4, ranks, p, st);
+                                    static_cast<size_t>(kDownWarps) * kDownTokens * (8 * NT + 1) * 4, ranks, false, p, st);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (p.n + kOutCols - 1) / kOutCols + (p.k + kOutCols - 1) / kOutCols;
     ranks = split_ranks(tiles, NT > 4 ? sms : 2 * sms, (p.M + 16 * kTokWarps - 1) / (16 * kTokWarps));
     if (tiles * ranks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     return launch_clusters(k_outer<NT, kDrop, kAligned>, dim3(static_cast<unsigned>(tiles * ranks), 1, 1), kOutThreads,
-                           static_cast<size_t>(8 * NT) * kOutRow * 4, ranks, p, st);
+                           static_cast<size_t>(8 * NT) * kOutRow * 4, ranks, true, p, st);
 }
 
 template <int NT>

@@ -25,6 +25,7 @@
 
 #include "act8.cuh"
 #include "act8.h"
+#include "dependent.cuh"
 #include "dropout.cuh"
 #include "host_cache.h"
 #include "sm100.cuh"
@@ -267,6 +268,8 @@ __device__ __forceinline__ bool feed(int steps, int &ci, Ring &c, int slots, uin
 // and `put(batch, group, values)` stores them. In the converting warps themselves the loads' latency showed in every fourth step.
 constexpr int kBatch = 4, kBatches = 3;
 
+__device__ __forceinline__ uint64_t pair(uint2 v) { return static_cast<uint64_t>(v.y) << 32 | v.x; }
+
 template <int kN, int kGroups, typename At, typename Put>
 __device__ __forceinline__ bool load_absmax(int steps, uint32_t afull, uint32_t aempty, int lane, At &&at, Put &&put) {
     Ring b;
@@ -280,7 +283,7 @@ __device__ __forceinline__ bool load_absmax(int steps, uint32_t afull, uint32_t 
             const uint16_t *p = at(i, 32 * g + lane, count);
             v[g] = 0;
             if (count >= kN && (reinterpret_cast<uintptr_t>(p) & (2u * kN - 1u)) == 0)
-                v[g] = kN == 4 ? __ldg(reinterpret_cast<const unsigned long long *>(p)) : ld_ro_u32(p);
+                v[g] = kN == 4 ? pair(ld_nc_v2(p)) : ld_nc_u32(p);
             else if (count > 0)
                 rest = true;
         }
@@ -292,7 +295,7 @@ __device__ __forceinline__ bool load_absmax(int steps, uint32_t afull, uint32_t 
                 if (count >= kN && (reinterpret_cast<uintptr_t>(p) & (2u * kN - 1u)) == 0) continue;
                 uint32_t w[kN];
 #pragma unroll
-                for (int e = 0; e < kN; ++e) w[e] = e < count ? ld_ro_u16(p + e) : 0u;
+                for (int e = 0; e < kN; ++e) w[e] = e < count ? ld_nc_u16(p + e) : 0u;
 #pragma unroll
                 for (int e = 0; e < kN; ++e) v[g] |= static_cast<uint64_t>(w[e]) << (16 * e);
             }
@@ -376,7 +379,7 @@ __device__ __forceinline__ void down_tc(const CUtensorMap *act, const CUtensorMa
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *slot;
-    grid_dependents_launch();
+    begin_dependent();  // the second kernel reads x and grad_h before its own wait: only once the first is past this
     // The tensor core cuts off what it adds instead of rounding it, so a long chain of MMAs drifts (448 of them: 1.6e-5
     // of the sum). So there are four accumulators, taken in turn and added up in fp32 registers by the other warps: of x,
     // whose codes go in as they are, one for each 64 features, times a / 128; of grad_h, one for each kSegment stages.
@@ -1058,7 +1061,7 @@ bool make_map(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, bool
 }
 
 template <typename K>
-cudaError_t launch_clusters(K kern, dim3 grid, int threads, size_t smem, int ranks, bool dependent, const CUtensorMap &a,
+cudaError_t launch_clusters(K kern, dim3 grid, int threads, size_t smem, int ranks, const CUtensorMap &a,
                             const CUtensorMap &b, const CUtensorMap &c, const CUtensorMap &d, const TcArgs &p,
                             cudaStream_t st) {
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kern), smem);
@@ -1076,7 +1079,7 @@ cudaError_t launch_clusters(K kern, dim3 grid, int threads, size_t smem, int ran
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = dependent ? 2 : 1;
+    cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, kern, a, b, c, d, p);
     if (e == cudaSuccess) count_launch();
     return e;
@@ -1229,13 +1232,13 @@ cudaError_t launch_act8_grads_tc(const int8_t *codes, const uint16_t *absmax, co
                                  : (p.rp > 32 ? k_down_tc<false, 4> : k_down_tc<false, 2>);
         const auto outer = masked ? k_outer_tc<true> : k_outer_tc<false>;
         const auto grid = [](int64_t n, int c, unsigned y) { return dim3(static_cast<unsigned>(n * c), y, 1); };
-        e = launch_clusters(down, grid(tok, rd, 2), kDownThreads, kDownSmem, rd, false, tm_gh, tm_codes, tm_A, tm_B, p, st);
+        e = launch_clusters(down, grid(tok, rd, 2), kDownThreads, kDownSmem, rd, tm_gh, tm_codes, tm_A, tm_B, p, st);
         p.tile0 = 0;
         if (e == cudaSuccess)
-            e = launch_clusters(outer, grid(so.first, so.c, 1), kOutThreads, kOutSmem, so.c, true, tm_gh, tm_codes, tm_t, tm_u, p, st);
+            e = launch_clusters(outer, grid(so.first, so.c, 1), kOutThreads, kOutSmem, so.c, tm_gh, tm_codes, tm_t, tm_u, p, st);
         p.tile0 = so.first;
         if (e == cudaSuccess && so.first < tiles)
-            e = launch_clusters(outer, grid(tiles - so.first, so.c_rest, 1), kOutThreads, kOutSmem, so.c_rest, true, tm_gh, tm_codes,
+            e = launch_clusters(outer, grid(tiles - so.first, so.c_rest, 1), kOutThreads, kOutSmem, so.c_rest, tm_gh, tm_codes,
                                 tm_t, tm_u, p, st);
         if (e != cudaSuccess) return e;
     }

@@ -12,6 +12,7 @@
 // which share its minimum and maximum by shuffles. k % group == 0, so groups do not straddle rows and
 // the matrix is walked as one flat array.
 #include "common.cuh"
+#include "dependent.cuh"
 #include "int4.h"
 
 namespace qn {
@@ -82,6 +83,7 @@ __global__ void __launch_bounds__(kThreads) k_int4_quantize(const uint16_t *W, i
                                                             uint16_t *scale, uint8_t *zero_point) {
     constexpr int kLanes = kGroup / 8;
     const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kThreads * kUnroll) + threadIdx.x;
+    begin_dependent();
     uint4 v[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -115,6 +117,7 @@ __global__ void __launch_bounds__(kThreads) k_int4_dequantize(const uint32_t *co
                                                               const uint8_t *zero_point, int64_t words, int shift,
                                                               uint16_t *out) {
     const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kThreads * kUnroll) + threadIdx.x;
+    begin_dependent();
     uint32_t c[kUnroll];
     float s[kUnroll], z[kUnroll];
 #pragma unroll
@@ -122,8 +125,8 @@ __global__ void __launch_bounds__(kThreads) k_int4_dequantize(const uint32_t *co
         const int64_t i = i0 + u * kThreads;
         const bool live = i < words;
         c[u] = live ? ld_nc_u32(codes + i) : 0u;
-        s[u] = __uint_as_float((live ? static_cast<uint32_t>(ld_ro_u16(scale + (i >> shift))) : 0u) << 16);
-        z[u] = live && zero_point ? static_cast<float>(__ldg(zero_point + (i >> shift))) : 8.0f;
+        s[u] = __uint_as_float((live ? ld_nc_u16(scale + (i >> shift)) : 0u) << 16);
+        z[u] = live && zero_point ? static_cast<float>(ld_nc_u8(zero_point + (i >> shift))) : 8.0f;
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -142,12 +145,10 @@ __global__ void __launch_bounds__(kThreads) k_int4_dequantize(const uint32_t *co
 }
 
 template <int kGroup>
-void quantize(const uint16_t *W, const Int4View &w, int64_t words, unsigned grid, cudaStream_t st) {
+cudaError_t quantize(const uint16_t *W, const Int4View &w, int64_t words, unsigned grid, cudaStream_t st) {
     uint32_t *codes = reinterpret_cast<uint32_t *>(w.codes);
-    if (w.zero_point)
-        k_int4_quantize<kGroup, true><<<grid, kThreads, 0, st>>>(W, words, codes, w.scale, w.zero_point);
-    else
-        k_int4_quantize<kGroup, false><<<grid, kThreads, 0, st>>>(W, words, codes, w.scale, nullptr);
+    return launch_dependent(w.zero_point ? k_int4_quantize<kGroup, true> : k_int4_quantize<kGroup, false>, grid, kThreads, st, W,
+                            words, codes, w.scale, w.zero_point);
 }
 
 bool grid_for(int64_t words, unsigned *grid) {
@@ -162,14 +163,8 @@ cudaError_t launch_int4_quantize(const uint16_t *W, const Int4View &w, cudaStrea
     const int64_t words = w.n * w.k / 8;
     unsigned grid;
     if (!grid_for(words, &grid)) return cudaErrorInvalidConfiguration;
-    if (w.group == 32)
-        quantize<32>(W, w, words, grid, st);
-    else if (w.group == 64)
-        quantize<64>(W, w, words, grid, st);
-    else
-        quantize<128>(W, w, words, grid, st);
-    count_launch();
-    return cudaGetLastError();
+    return w.group == 32 ? quantize<32>(W, w, words, grid, st)
+                         : w.group == 64 ? quantize<64>(W, w, words, grid, st) : quantize<128>(W, w, words, grid, st);
 }
 
 cudaError_t launch_int4_dequantize(const Int4View &w, uint16_t *out, cudaStream_t st) {
@@ -177,10 +172,8 @@ cudaError_t launch_int4_dequantize(const Int4View &w, uint16_t *out, cudaStream_
     unsigned grid;
     if (!grid_for(words, &grid)) return cudaErrorInvalidConfiguration;
     const int shift = w.group == 32 ? 2 : w.group == 64 ? 3 : 4;
-    k_int4_dequantize<<<grid, kThreads, 0, st>>>(reinterpret_cast<const uint32_t *>(w.codes), w.scale, w.zero_point,
-                                                 words, shift, out);
-    count_launch();
-    return cudaGetLastError();
+    return launch_dependent(k_int4_dequantize, grid, kThreads, st, reinterpret_cast<const uint32_t *>(w.codes), w.scale,
+                            w.zero_point, words, shift, out);
 }
 
 }  // namespace qn

@@ -25,6 +25,7 @@
 // instructions for 8 weights of a row: the integer pipe and the waits between dependent instructions bound the
 // large call (43 % of issue slots), start-up, the sums across CTAs and the copy of x the small ones.
 #include "common.cuh"
+#include "dependent.cuh"
 #include "host_cache.h"
 #include "int4.h"
 #include "stream_common.cuh"
@@ -108,8 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_int4_linear(const LinArgs p) {
     const int x_len = static_cast<int>(steps * (slice + 1) / S - x0);
     const int64_t groups = p.k / (32 * kWords);
 
-    grid_dependents_launch();
-    grid_dependency_wait();
+    begin_dependent();
 
     // x of the CTA's steps: [step][word of a lane][token][t] x 16 bytes, zeros past k
     {
@@ -185,12 +185,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_int4_linear(const LinArgs p) {
 #pragma unroll
         for (int j = 0; j < kGroups; ++j) {
             const bool in = 4 * j + t < count * kGroups && 4 * j + t < left;
-            sa[j] = in ? ld_ro_u16(p.scale + ia + 4 * j) : 0u;
-            sb[j] = in ? ld_ro_u16(p.scale + ib + 4 * j) : 0u;
+            sa[j] = in ? ld_nc_u16(p.scale + ia + 4 * j) : 0u;
+            sb[j] = in ? ld_nc_u16(p.scale + ib + 4 * j) : 0u;
             za[j] = zb[j] = 8u;
             if (kZero) {
-                za[j] = in ? __ldg(p.zero_point + ia + 4 * j) : 0u;
-                zb[j] = in ? __ldg(p.zero_point + ib + 4 * j) : 0u;
+                za[j] = in ? ld_nc_u8(p.zero_point + ia + 4 * j) : 0u;
+                zb[j] = in ? ld_nc_u8(p.zero_point + ib + 4 * j) : 0u;
             }
         }
     };

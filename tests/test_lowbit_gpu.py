@@ -587,6 +587,24 @@ def test_calls_side_by_side_on_two_streams():
         assert all(torch.equal(a, b) for g in got[i] for a, b in zip(g, want[i]))
 
 
+@pytest.mark.parametrize("rows,cols", [(3, 192), (700, 4096)])
+def test_back_to_back_launches_see_what_the_one_before_wrote(rows, cols):
+    # one set of buffers in turn: a kernel may be set up, but not read or write, before the one before it is done
+    xs = [rand(rows, cols, std=0.02 * (i + 1), seed=i) for i in range(8)]
+    W = [rand(256, cols, std=0.02, seed=i) for i in range(8)]
+    want = [(qb.act8_dequantize(qb.act8_quantize(x)), qb.int4_linear_fwd(qb.int4_quantize(w, group=64), x[:3]),
+             qb.int4_dequantize(qb.int4_quantize(w, group=64))) for x, w in zip(xs, W)]
+    torch.cuda.synchronize()
+    a, w = qb.Act8.empty(rows, cols), qb.Int4Weight.empty(256, cols, 64)
+    got = []
+    for x, v in zip(xs * 4, W * 4):
+        qb.act8_quantize(x, out=a)
+        y = qb.act8_dequantize(a)
+        qb.int4_quantize(v, out=w)
+        got.append((y, qb.int4_linear_fwd(w, x[:3]), qb.int4_dequantize(w)))
+    assert all(torch.equal(p, q) for i, g in enumerate(got) for p, q in zip(g, want[i % 8]))
+
+
 def test_results_do_not_land_in_memory_that_the_current_stream_still_uses():
     x, w = rand(64, 640, seed=1), random_int4(64, 640, 64, True, seed=2)
     want_a, want_h = qb.act8_quantize(x).codes, qb.int4_linear_fwd(w, x)
