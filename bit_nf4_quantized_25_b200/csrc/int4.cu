@@ -23,57 +23,92 @@ constexpr int kThreads = 256;
 constexpr int kUnroll = 4;
 constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it leaves an integer in the low mantissa bits
 
-// Scale, zero point and codes of a lane's 8 weights; all lanes of the warp call it.
-//
-// The quotient w / s is taken as w inv with inv = fl32((1 + 2^-17) / s): w and s have 8-bit
-// significands, so a quotient that is not a half is at least 1 / 512 of a unit away from one, and one
-// that is a half is raised above it by more than the rounding of inv; at up to 16 units the raise is
-// below 2^-13. An fma onto 1.5 * 2^23 + z then gives round(w / s) + z with halves away from zero.
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {  // of bf16 pairs
+    const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&m);
+}
+
+// A group's largest weight and the size of its smallest, both at least 0, or (not kZero) its largest size; all lanes of the
+// warp call it. Both run through one bf16 pair: (max w, max -w).
 template <int kGroup, bool kZero>
-__device__ __forceinline__ uint32_t encode(const uint4 &v, uint32_t &scale_bits, int &zero) {
-    constexpr int kLanes = kGroup / 8;
+__device__ __forceinline__ void range(const uint4 &v, float &hi, float &below) {
+    constexpr uint32_t kSigns = 0x80008000u;
+    uint32_t m;
+    if (kZero) {
+        const uint32_t a = max2(max2(v.x, v.y), max2(v.z, v.w));
+        const uint32_t b = max2(max2(v.x ^ kSigns, v.y ^ kSigns), max2(v.z ^ kSigns, v.w ^ kSigns));
+        m = max2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+    } else {
+        m = max2(max2(v.x & ~kSigns, v.y & ~kSigns), max2(v.z & ~kSigns, v.w & ~kSigns));
+    }
+#pragma unroll
+    for (int d = 1; d < kGroup / 8; d <<= 1) m = max2(m, __shfl_xor_sync(0xffffffffu, m, d));
+    m = max2(m, 0u);
+    hi = bf16_lo(m);
+    below = bf16_hi(m);
+    if (!kZero) hi = fmaxf(hi, below);
+}
+
+// Scale, zero point and codes of a lane's 8 weights in a group with this range.
+//
+// The quotient w / s is taken as w inv with inv = (1 + 2^-17) / s to 2^-21 of itself: w and s have 8-bit
+// significands, so a quotient that is not a half is at least 1 / 512 of a unit away from one, and one
+// that is a half is raised above it by more than the error of inv; at up to 16 units the raise is
+// below 2^-12. An fma onto 1.5 * 2^23 + z then gives round(w / s) + z with halves away from zero.
+template <bool kZero>
+__device__ __noinline__ uint4 encode_any(uint4 v, float hi, float below) {  // codes, scale, zero point
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-    float w[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        w[2 * i] = bf16_lo(u[i]);
-        w[2 * i + 1] = bf16_hi(u[i]);
-    }
-    float lo = 0.0f, hi = 0.0f;  // kZero: minimum and maximum with 0; else hi is max |w|
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (kZero) lo = fminf(lo, w[i]);
-        hi = fmaxf(hi, kZero ? w[i] : fabsf(w[i]));
-    }
-#pragma unroll
-    for (int d = 1; d < kLanes; d <<= 1) {
-        if (kZero) lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, d));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, d));
-    }
-    float span = hi - lo;
-    if (kZero && span > 3.4028235e38f) span = 2.0f * __fdiv_rn(0.5f * hi - 0.5f * lo, 15.0f);  // hi - lo overflowed
+    float span = kZero ? hi + below : hi;
+    if (kZero && span > 3.4028235e38f) span = 2.0f * __fdiv_rn(0.5f * hi + 0.5f * below, 15.0f);  // hi + below overflowed
     else span = __fdiv_rn(span, kZero ? 15.0f : 7.0f);
-    scale_bits = __bfloat16_as_ushort(__float2bfloat16_rn(span));
-    float s = __uint_as_float(scale_bits << 16);
-    if (s == 0.0f) {
-        zero = kZero ? 0 : 8;
-        return kZero ? 0u : 0x88888888u;
-    }
-    if (s < 0x1p-100f) {  // keep 1 / s finite: w / s of both times 2^64, exact
-        s *= 0x1p64f;
-        lo *= 0x1p64f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] *= 0x1p64f;
-    }
-    const float inv = __fdiv_rn(0x1.0001p+0f, s);
-    zero = 8;
-    if (kZero) zero = min(static_cast<int>(__float_as_uint(__fmaf_rn(-lo, inv, kMagic)) - 0x4b400000u), 15);
-    const float base = kMagic + static_cast<float>(zero);
+    const uint32_t scale_bits = __bfloat16_as_ushort(__float2bfloat16_rn(span));
+    float s = __uint_as_float(scale_bits << 16), times = 1.0f;
+    if (s == 0.0f) return kZero ? make_uint4(0u, scale_bits, 0u, 0u) : make_uint4(0x88888888u, scale_bits, 8u, 0u);
+    if (s < 0x1p-80f) times = 0x1p64f;  // keep 1 / s finite: w / s of both times 2^64, exact
+    const float inv = __fdiv_rn(0x1.0001p+0f, s * times);
+    int z = 8;
+    if (kZero) z = min(static_cast<int>(__float_as_uint(__fmaf_rn(below * times, inv, kMagic)) - 0x4b400000u), 15);
+    const float base = kMagic + static_cast<float>(z);
     uint32_t word = 0u;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int q = static_cast<int>(__float_as_uint(__fmaf_rn(w[i], inv, base)) - 0x4b400000u);
+        const float w = (i & 1 ? bf16_hi(u[i / 2]) : bf16_lo(u[i / 2])) * times;
+        const int q = static_cast<int>(__float_as_uint(__fmaf_rn(w, inv, base)) - 0x4b400000u);
         word |= static_cast<uint32_t>(min(max(q, 0), 15)) << (4 * i);
+    }
+    return make_uint4(word, scale_bits, static_cast<uint32_t>(z), 0u);
+}
+
+// The same for ordinary ranges, in a third of the instructions (with encode_any for all the kernel was bound by issuing them:
+// 28672 x 8192 took 131 us). span / 15 (7) is the product with the reciprocal and one correction by its remainder, which
+// rounds as the division does (Markstein's theorem; checked for every significand). s is then span / 15 (7) to 2^-8.9 of itself, so
+// w / s is above -z - 1/2 and, without zero points, within 7.1: only w / s + z with zero points can come out above 15, by 1.
+template <bool kZero>
+__device__ __forceinline__ uint32_t encode(const uint4 &v, float hi, float below, uint32_t &scale_bits, uint32_t &zero) {
+    const float span = kZero ? hi + below : hi;
+    if (!(span > 0x1p-60f && span < 0x1p120f)) {
+        const uint4 r = encode_any<kZero>(v, hi, below);
+        scale_bits = r.y;
+        zero = r.z;
+        return r.x;
+    }
+    constexpr float kSteps = kZero ? 15.0f : 7.0f, kOver = 1.0f / kSteps;
+    const float near = span * kOver, fl = __fmaf_rn(__fmaf_rn(-kSteps, near, span), kOver, near);
+    scale_bits = __bfloat16_as_ushort(__float2bfloat16_rn(fl));
+    const float inv = __fdividef(0x1.0001p+0f, __uint_as_float(scale_bits << 16));
+    float base = kMagic + 8.0f;
+    zero = 8u;
+    if (kZero) {
+        base = __fmaf_rn(below, inv, kMagic);
+        zero = __float_as_uint(base) & 15u;
+    }
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    uint32_t word = 0u - 0x4b400000u * 0x11111111u;  // the sums' leading bits, which fall out
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float q = __fmaf_rn(i & 1 ? bf16_hi(u[i / 2]) : bf16_lo(u[i / 2]), inv, base);
+        if (kZero) q = fminf(q, kMagic + 15.0f);
+        word += __float_as_uint(q) << (4 * i);
     }
     return word;
 }
@@ -93,9 +128,10 @@ __global__ void __launch_bounds__(kThreads) k_int4_quantize(const uint16_t *W, i
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
         const int64_t i = i0 + u * kThreads;
-        uint32_t sb;
-        int z;
-        const uint32_t word = encode<kGroup, kZero>(v[u], sb, z);
+        uint32_t sb, z;
+        float hi, below;
+        range<kGroup, kZero>(v[u], hi, below);
+        const uint32_t word = encode<kZero>(v[u], hi, below, sb, z);
         if (i >= words) continue;
         codes[i] = word;
         if ((threadIdx.x & (kLanes - 1)) == 0) {
