@@ -403,6 +403,22 @@ def test_int4_halves_constants_and_extremes():
         assert bool(back.isfinite().all()) and float((back - W[7:8].double()).abs().max()) <= 0.5625 * step
 
 
+@pytest.mark.parametrize("exponent", [0, 100, 119, -55, -57, -100, -120])
+def test_int4_every_pair_of_range_significands(exponent):
+    # groups of 64 from -b to a for each of the 128 significands of a and of b (a sixteenth, half, twice and as large), with
+    # weights at multiples of half a step; the exponents lie on both sides of what is an ordinary range
+    g = torch.Generator().manual_seed(exponent % 1000)
+    a = (1.0 + torch.arange(128) / 128.0).view(-1, 1).expand(128, 128)
+    b = (1.0 + torch.arange(128) / 128.0).view(1, -1) * torch.tensor([1.0, 0.0625, 0.5, 2.0])[torch.randint(0, 4, (128, 128), generator=g)]
+    half = ((a + b) / 30.0).unsqueeze(-1)
+    low = -(b.unsqueeze(-1) / half).floor()
+    k = low + (torch.rand(128, 128, 62, generator=g) * ((a.unsqueeze(-1) / half).floor() - low)).round()
+    W = torch.cat([a.unsqueeze(-1), -b.unsqueeze(-1), (k * half).clamp(-b.unsqueeze(-1), a.unsqueeze(-1))], -1)
+    W = (W.double() * 2.0 ** exponent).reshape(128, -1).to(BF).to(DEV)
+    check_int4(W, 64, True)
+    check_int4(W, 64, False)
+
+
 def test_int4_writes_only_its_buffers():
     n, k, group = 5, 384, 64
     W = rand(n, k, std=0.02, seed=1)
