@@ -9,9 +9,8 @@
 // rounded before the one rounding of h.
 //
 // The order of k inside a group is free as long as A and B agree, so lane (g, t) of a warp takes a quarter t of
-// the group of rows g and g + 8 as whole words: 32-bit words of 8 weights, whose nibbles p and p + 4 are a pair
-// ((word >> 4p) & 0x000f000f | 0x43004300 is the bf16 pair 128 + q; minus 128 + z is exact). One word of each
-// row feeds two MMAs. x is paired the same way once, when a CTA copies its part of it to shared memory.
+// the group of rows g and g + 8 as whole words: 32-bit words of 8 weights, whose nibbles p and p + 4 are a pair (see
+// unpack). One word of each row feeds two MMAs. x is paired the same way once, when a CTA copies its part of it to shared memory.
 //
 // A cluster has a range of 16-row tiles, its CTAs (slices) split k. A CTA keeps its part of x, all of it, in shared
 // memory, so x is read from L2 once per CTA: all SMs ask for the same lines of it at about the same time, and with x from
@@ -20,10 +19,11 @@
 // warp has kSlots steps of its weights in flight, in a ring of its own: asynchronous copies, since loads to registers
 // that are waited for one by one end up waiting for the youngest. The parts' sums meet in shared memory.
 //
-// Measured (weights with scales and zero points of 128, resp. 32): 4096 x 4096, 1 token 6.7 us, 11008 x 4096, 5 tokens
-// 14.5 us, 8192 x 28672, 16 tokens 61.8 us (2.0 TB/s). Three quarters of the warps' time is the unpacking, 10
-// instructions for 8 weights of a row: the integer pipe and the waits between dependent instructions bound the
-// large call (43 % of issue slots), start-up, the sums across CTAs and the copy of x the small ones.
+// Measured, with zero points: 4096 x 4096 (group 128) 1 token 6.7 us; 8192 x 28672 (128) 1, 8 and 16 tokens 34.7, 41.4 and
+// 58.8 us (3.5, 3.0 and 2.1 TB/s); 11008 x 4096 (32) 5 tokens 14.2 us. Three quarters of the warps' time goes by in the
+// loop, 190 instructions of a warp for 16 rows x 128 k at 16 tokens, and no pipe is busy for a third of it: waits between
+// dependent instructions bound it, four warps to a scheduler. x of 16 tokens leaves no room for more, and 120 of 148 SMs hold
+// the clusters of 8 that it needs. Small calls are start-up, the copy of x and the sums across CTAs.
 #include "common.cuh"
 #include "dependent.cuh"
 #include "host_cache.h"
@@ -54,8 +54,9 @@ struct LinArgs {
     int slices;     // CTAs of a cluster
 };
 
-__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
-    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+    const __nv_bfloat162 d = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b),
+                                     *reinterpret_cast<const __nv_bfloat162 *>(&c));
     return *reinterpret_cast<const uint32_t *>(&d);
 }
 
@@ -72,12 +73,19 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t *w) {
     }
 }
 
-// (w & 0x000f000f) | 0x43004300 in one instruction
-__device__ __forceinline__ uint32_t nibbles(uint32_t w, uint32_t mask, uint32_t base) {
-    uint32_t d;
-    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(w), "r"(mask), "r"(base));
-    return d;
+// A word's 8 codes less z, in pairs p and p + 4, times kUnit: as a bf16, bits 0..3 are q 2^-133 and bits 4..7 q 2^-129
+// (subnormal), so a multiplication brings both to q 2^-6. nz: -z 2^-6. All exact.
+constexpr float kUnit = 0x1p-6f;
+constexpr uint32_t kTo6 = 0x7f007f00u, kTo6High = 0x7d007d00u;  // 2^127, 2^123
+__device__ __forceinline__ void unpack(uint32_t w, uint32_t nz, uint32_t (&a)[4]) {
+    const uint32_t h = w >> 8;
+    a[0] = fma_bf16x2(w & 0x000f000fu, kTo6, nz);
+    a[1] = fma_bf16x2(w & 0x00f000f0u, kTo6High, nz);
+    a[2] = fma_bf16x2(h & 0x000f000fu, kTo6, nz);
+    a[3] = fma_bf16x2(h & 0x00f000f0u, kTo6High, nz);
 }
+// -z 2^-6 twice, of the low byte of v.
+__device__ __forceinline__ uint32_t minus_zero(uint32_t v) { return fma_bf16x2(__byte_perm(v, 0u, 0x4040), kTo6 | 0x80008000u, 0x80008000u); }
 
 __device__ __forceinline__ float ld_cluster(uint32_t addr) {
     float v;
@@ -252,14 +260,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_int4_linear(const LinArgs p) {
                 }
                 sum += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
             }
-            p.h[m * p.n + row0 + r] = __bfloat16_as_ushort(__float2bfloat16_rn(sum));
+            p.h[m * p.n + row0 + r] = __bfloat16_as_ushort(__float2bfloat16_rn(sum * (1.0f / kUnit)));
         }
         __syncwarp();
     };
 
     // tokens past the end have whatever lies there and are not stored
     const uint32_t x_lane = xs + static_cast<uint32_t>(g * 64 + t * 16);
-    const uint32_t kMask = 0x000f000fu, kBase = 0x43004300u;
     for (int batch = 0; batch < batches; ++batch) {
         float out[NT][4];
 #pragma unroll
@@ -300,18 +307,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_int4_linear(const LinArgs p) {
                         const int from = i * kGroups + e;
                         const uint32_t qa = __shfl_sync(0xffffffffu, pa[from / 4], from % 4, 4);
                         const uint32_t qb = __shfl_sync(0xffffffffu, pb[from / 4], from % 4, 4);
-                        // 128 + z as a bf16 pair
-                        const uint32_t oa = kZero ? __byte_perm(qa, 0x43u, 0x4040) : 0x43084308u;
-                        const uint32_t ob = kZero ? __byte_perm(qb, 0x43u, 0x4040) : 0x43084308u;
+                        const uint32_t oa = kZero ? minus_zero(qa) : 0xbe00be00u, ob = kZero ? minus_zero(qb) : 0xbe00be00u;
                         float acc[NT][4];
 #pragma unroll
                         for (int w = 0; w < kWords; ++w) {
                             uint32_t a[4], b[4];
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                a[q] = sub_bf16x2(nibbles(wa[e * kWords + w] >> (4 * q), kMask, kBase), oa);
-                                b[q] = sub_bf16x2(nibbles(wb[e * kWords + w] >> (4 * q), kMask, kBase), ob);
-                            }
+                            unpack(wa[e * kWords + w], oa, a);
+                            unpack(wb[e * kWords + w], ob, b);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
                                 const uint4 v = stream::lds128(xa + i * kXStep + (e * kWords + w) * kWordBytes + nt * 512);
