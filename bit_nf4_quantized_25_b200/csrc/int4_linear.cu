@@ -84,8 +84,8 @@ __device__ __forceinline__ void unpack(uint32_t w, uint32_t nz, uint32_t (&a)[4]
     a[2] = fma_bf16x2(h & 0x000f000fu, kTo6, nz);
     a[3] = fma_bf16x2(h & 0x00f000f0u, kTo6High, nz);
 }
-// -z 2^-6 twice, of the low byte of v.
-__device__ __forceinline__ uint32_t minus_zero(uint32_t v) { return fma_bf16x2(__byte_perm(v, 0u, 0x4040), kTo6 | 0x80008000u, 0x80008000u); }
+// -z 2^-6 in the lower half.
+__device__ __forceinline__ uint32_t minus_zero(uint32_t z) { return fma_bf16x2(z, kTo6 | 0x80008000u, 0x80008000u); }
 
 __device__ __forceinline__ float ld_cluster(uint32_t addr) {
     float v;
@@ -195,7 +195,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_int4_linear(const LinArgs p) {
             const bool in = 4 * j + t < count * kGroups && 4 * j + t < left;
             sa[j] = in ? ld_nc_u16(p.scale + ia + 4 * j) : 0u;
             sb[j] = in ? ld_nc_u16(p.scale + ib + 4 * j) : 0u;
-            za[j] = zb[j] = 8u;
             if (kZero) {
                 za[j] = in ? ld_nc_u8(p.zero_point + ia + 4 * j) : 0u;
                 zb[j] = in ? ld_nc_u8(p.zero_point + ib + 4 * j) : 0u;
@@ -277,8 +276,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_int4_linear(const LinArgs p) {
             uint32_t pa[kGroups], pb[kGroups];
 #pragma unroll
             for (int j = 0; j < kGroups; ++j) {
-                pa[j] = sa[j] << 16 | za[j];
-                pb[j] = sb[j] << 16 | zb[j];
+                pa[j] = sa[j] << 16 | (kZero ? minus_zero(za[j]) & 0xffffu : 0u);
+                pb[j] = sb[j] << 16 | (kZero ? minus_zero(zb[j]) & 0xffffu : 0u);
             }
             // what is copied next: the next unit of this part, or the first of the next batch's
             int ahead = left_len - kSlots;
@@ -307,7 +306,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_int4_linear(const LinArgs p) {
                         const int from = i * kGroups + e;
                         const uint32_t qa = __shfl_sync(0xffffffffu, pa[from / 4], from % 4, 4);
                         const uint32_t qb = __shfl_sync(0xffffffffu, pb[from / 4], from % 4, 4);
-                        const uint32_t oa = kZero ? minus_zero(qa) : 0xbe00be00u, ob = kZero ? minus_zero(qb) : 0xbe00be00u;
+                        const uint32_t oa = kZero ? __byte_perm(qa, qa, 0x1010) : 0xbe00be00u;
+                        const uint32_t ob = kZero ? __byte_perm(qb, qb, 0x1010) : 0xbe00be00u;
                         float acc[NT][4];
 #pragma unroll
                         for (int w = 0; w < kWords; ++w) {
