@@ -38,8 +38,7 @@ struct GradArgs {
     int64_t M, n, k;
     const uint16_t *A;  // r x k
     const uint16_t *B;  // n x r
-    int r;              // all of the rank; this launch takes j0 .. j0 + 8 NT
-    int j0;
+    int r;
     float s;
     float *grad_A, *grad_B;
     float *t, *u;  // fragment order, see frag_index
@@ -107,17 +106,7 @@ constexpr int kPiece = 64;  // features per step of a warp
 template <int NT>
 __device__ __forceinline__ void load_js(const uint16_t *p, int count, bool vec, uint32_t (&w)[(NT + 1) / 2]) {
     if (vec && count >= NT) {
-        if constexpr (NT == 8) {
-            const uint4 v = ld_ro_v4(p);
-            w[0] = v.x;
-            w[1] = v.y;
-            w[2] = v.z;
-            w[3] = v.w;
-        } else if constexpr (NT == 4) {
-            const uint2 v = ld_ro_v2(p);
-            w[0] = v.x;
-            w[1] = v.y;
-        } else if constexpr (NT == 2) {
+        if constexpr (NT == 2) {
             w[0] = ld_ro_u32(p);
         } else {
             w[0] = ld_ro_u16(p);
@@ -139,7 +128,7 @@ __device__ __forceinline__ void load_js(const uint16_t *p, int count, bool vec, 
 //           permutes
 // Column g of the MMA's tile nt is j = NT g + nt.
 template <int NT, bool kX, bool kDrop>
-__device__ __forceinline__ void down(const GradArgs &p, float *red, int64_t tile, uint32_t rank, uint32_t ranks) {
+__device__ __forceinline__ void down(const GradArgs &p, float *red, int j0, int64_t tile, uint32_t rank, uint32_t ranks) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int64_t m0 = tile * kDownTokens;
     const int64_t width = kX ? p.k : p.n, pieces = (width + kPiece - 1) / kPiece;
@@ -150,7 +139,7 @@ __device__ __forceinline__ void down(const GradArgs &p, float *red, int64_t tile
         live[h] = m0 + g + 8 * h < p.M;
         row[h] = live[h] ? m0 + g + 8 * h : 0;
     }
-    const int js = p.r - p.j0 < 8 * NT ? p.r - p.j0 : 8 * NT;  // columns of this pass
+    const int js = p.r - j0 < 8 * NT ? p.r - j0 : 8 * NT;  // columns of this block
     const bool vec = p.r % NT == 0;
 
     float acc[2][NT][4];
@@ -193,7 +182,7 @@ __device__ __forceinline__ void down(const GradArgs &p, float *red, int64_t tile
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const int j = NT * g + nt;
-                    const uint4 f = j < js ? ld_ro_v4(p.A + static_cast<int64_t>(p.j0 + j) * p.k + c0 + 32 * sub) : make_uint4(0u, 0u, 0u, 0u);
+                    const uint4 f = j < js ? ld_ro_v4(p.A + static_cast<int64_t>(j0 + j) * p.k + c0 + 32 * sub) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
                     for (int mt = 0; mt < 2; ++mt) {
                         mma_16816(d[mt][nt], a[2 * mt][0], a[2 * mt + 1][0], a[2 * mt][1], a[2 * mt + 1][1], f.x, f.y);
@@ -225,7 +214,7 @@ __device__ __forceinline__ void down(const GradArgs &p, float *red, int64_t tile
                 }
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    load_js<NT>(p.B + (c0 + q) * p.r + p.j0 + NT * g, c0 + q < p.n ? js - NT * g : 0, vec, w[q]);
+                    load_js<NT>(p.B + (c0 + q) * p.r + j0 + NT * g, c0 + q < p.n ? js - NT * g : 0, vec, w[q]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const uint32_t sel = (nt & 1) ? 0x7632 : 0x5410;
@@ -267,7 +256,7 @@ __device__ __forceinline__ void down(const GradArgs &p, float *red, int64_t tile
         __syncthreads();
     }
     float *out = kX ? p.t : p.u;
-    const int jt_all = (p.r + 7) / 8, jt0 = p.j0 / 8;
+    const int jt_all = (p.r + 7) / 8, jt0 = j0 / 8;
     constexpr int kAll = kDownTokens / 16 * NT * 128;
     const int e0 = static_cast<int>(kAll * rank / ranks), e1 = static_cast<int>(kAll * (rank + 1) / ranks);
     for (int e = e0 + threadIdx.x; e < e1; e += kDownThreads) {
@@ -288,17 +277,18 @@ __device__ __forceinline__ void down(const GradArgs &p, float *red, int64_t tile
     }
 }
 
-// grid (ranks * token tiles, 2): y = 0 takes u from grad_h, y = 1 t from the codes.
+// grid (ranks * token tiles, 2, blocks of 8 NT columns j): y = 0 takes u from grad_h, y = 1 t from the codes.
 template <int NT, bool kDrop>
 __global__ void __launch_bounds__(kDownThreads) k_down(const GradArgs p) {
     extern __shared__ __align__(16) float red[];
     const uint32_t rank = cluster_rank(), ranks = cluster_size();
     const int64_t tile = blockIdx.x / ranks;
     grid_dependents_launch();
+    const int j0 = static_cast<int>(blockIdx.z) * 8 * NT;
     if (blockIdx.y == 0)
-        down<NT, false, false>(p, red, tile, rank, ranks);
+        down<NT, false, false>(p, red, j0, tile, rank, ranks);
     else
-        down<NT, true, kDrop>(p, red, tile, rank, ranks);
+        down<NT, true, kDrop>(p, red, j0, tile, rank, ranks);
 }
 
 // -------------------------------------------------------------- products over tokens
@@ -322,12 +312,12 @@ __device__ __forceinline__ void split(float (&v)[4], uint32_t (&part)[3][2]) {
 }
 
 template <int NT, bool kX, bool kDrop, bool kAligned>
-__device__ __forceinline__ void outer(const GradArgs &p, float *red, int64_t tile, uint32_t rank, uint32_t ranks) {
+__device__ __forceinline__ void outer(const GradArgs &p, float *red, int j0, int64_t tile, uint32_t rank, uint32_t ranks) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int cw = warp % kColWarps, tw = warp / kColWarps;
     const int64_t width = kX ? p.k : p.n;
     const int64_t col0 = tile * kOutCols + 64 * cw, col = col0 + 8 * g;
-    const int jt_all = (p.r + 7) / 8, jt0 = p.j0 / 8;
+    const int jt_all = (p.r + 7) / 8, jt0 = j0 / 8;
     const float *R = kX ? p.u : p.t;
     const int64_t tiles16 = (p.M + 15) / 16;
 
@@ -439,7 +429,7 @@ __device__ __forceinline__ void outer(const GradArgs &p, float *red, int64_t til
         stream::cluster_arrive_release();
         stream::cluster_wait_acquire();
     }
-    const int js = p.r - p.j0 < 8 * NT ? p.r - p.j0 : 8 * NT;
+    const int js = p.r - j0 < 8 * NT ? p.r - j0 : 8 * NT;
     const int all = js * kOutCols;
     const int e0 = static_cast<int>(static_cast<int64_t>(all) * rank / ranks);
     const int e1 = static_cast<int>(static_cast<int64_t>(all) * (rank + 1) / ranks);
@@ -455,9 +445,9 @@ __device__ __forceinline__ void outer(const GradArgs &p, float *red, int64_t til
         else
             sum = *src;
         if (kX)
-            p.grad_A[static_cast<int64_t>(p.j0 + j) * p.k + cc] = p.s * sum;
+            p.grad_A[static_cast<int64_t>(j0 + j) * p.k + cc] = p.s * sum;
         else
-            p.grad_B[cc * p.r + p.j0 + j] = p.s * sum;
+            p.grad_B[cc * p.r + j0 + j] = p.s * sum;
     }
     if (ranks > 1) {
         stream::cluster_arrive_release();
@@ -465,23 +455,22 @@ __device__ __forceinline__ void outer(const GradArgs &p, float *red, int64_t til
     }
 }
 
-// Column tiles of grad_h first, then those of the codes.
+// grid (ranks * column tiles, blocks of 8 NT columns j): column tiles of grad_h first, then those of the codes.
 template <int NT, bool kDrop, bool kAligned>
 __global__ void __launch_bounds__(kOutThreads) k_outer(const GradArgs p) {
     extern __shared__ __align__(16) uint8_t smem[];
     const uint32_t rank = cluster_rank(), ranks = cluster_size();
     const int64_t tile = blockIdx.x / ranks, tiles_gh = (p.n + kOutCols - 1) / kOutCols;
+    const int j0 = static_cast<int>(blockIdx.y) * 8 * NT;
     if (tile < tiles_gh)
-        outer<NT, false, false, kAligned>(p, reinterpret_cast<float *>(smem), tile, rank, ranks);
+        outer<NT, false, false, kAligned>(p, reinterpret_cast<float *>(smem), j0, tile, rank, ranks);
     else
-        outer<NT, true, kDrop, true>(p, reinterpret_cast<float *>(smem), tile - tiles_gh, rank, ranks);
+        outer<NT, true, kDrop, true>(p, reinterpret_cast<float *>(smem), j0, tile - tiles_gh, rank, ranks);
 }
 
 template <typename K>
 cudaError_t launch_clusters(K kern, dim3 grid, int threads, size_t smem, int ranks, bool dependent, const GradArgs &p,
                             cudaStream_t st) {
-    cudaError_t e = smem > 48 * 1024 ? ensure_smem_limit(reinterpret_cast<const void *>(kern), smem) : cudaSuccess;
-    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
@@ -501,7 +490,7 @@ cudaError_t launch_clusters(K kern, dim3 grid, int threads, size_t smem, int ran
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
-    e = cudaLaunchKernelEx(&cfg, kern, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
     if (e == cudaSuccess) count_launch();
     return e;
 }
@@ -517,16 +506,17 @@ template <int NT, bool kDrop, bool kAligned>
 cudaError_t launch_pass(const GradArgs &p, int sms, cudaStream_t st) {
     const int64_t tok = (p.M + kDownTokens - 1) / kDownTokens;
     const int64_t rounds = ((p.n > p.k ? p.n : p.k) + kPiece * kDownWarps - 1) / (kPiece * kDownWarps);
-    int ranks = split_ranks(2 * tok, 2 * sms, rounds);
+    const int64_t js = (p.r + 8 * NT - 1) / (8 * NT);
+    int ranks = split_ranks(2 * tok * js, 2 * sms, rounds);
     if (tok * ranks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    cudaError_t e = launch_clusters(k_down<NT, kDrop>, dim3(static_cast<unsigned>(tok * ranks), 2, 1), kDownThreads,
-                                    static_cast<size_t>(kDownWarps) * kDownTokens * (8 * NT + 1) * 4, ranks, false, p, st);
+    cudaError_t e = launch_clusters(k_down<NT, kDrop>, dim3(static_cast<unsigned>(tok * ranks), 2, static_cast<unsigned>(js)),
+                                    kDownThreads, static_cast<size_t>(kDownWarps) * kDownTokens * (8 * NT + 1) * 4, ranks, false, p, st);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (p.n + kOutCols - 1) / kOutCols + (p.k + kOutCols - 1) / kOutCols;
-    ranks = split_ranks(tiles, NT > 4 ? sms : 2 * sms, (p.M + 16 * kTokWarps - 1) / (16 * kTokWarps));
+    ranks = split_ranks(tiles * js, 2 * sms, (p.M + 16 * kTokWarps - 1) / (16 * kTokWarps));
     if (tiles * ranks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    return launch_clusters(k_outer<NT, kDrop, kAligned>, dim3(static_cast<unsigned>(tiles * ranks), 1, 1), kOutThreads,
-                           static_cast<size_t>(8 * NT) * kOutRow * 4, ranks, true, p, st);
+    return launch_clusters(k_outer<NT, kDrop, kAligned>, dim3(static_cast<unsigned>(tiles * ranks), static_cast<unsigned>(js), 1),
+                           kOutThreads, static_cast<size_t>(8 * NT) * kOutRow * 4, ranks, true, p, st);
 }
 
 template <int NT>
@@ -557,21 +547,9 @@ cudaError_t launch_act8_grads(const int8_t *codes, const uint16_t *absmax, const
     int sms = 148;
     cudaError_t e = device_sm_count(&sms);
     if (e != cudaSuccess) return e;
-    GradArgs p{codes, absmax, gh, M, n, k, A, B, r, 0, s, grad_A, grad_B, static_cast<float *>(ws), nullptr, drop};
+    GradArgs p{codes, absmax, gh, M, n, k, A, B, r, s, grad_A, grad_B, static_cast<float *>(ws), nullptr, drop};
     p.u = p.t + (M + 15) / 16 * 16 * ((r + 7) / 8 * 8);
-    for (p.j0 = 0; p.j0 < r; p.j0 += 64) {
-        const int nt = (r - p.j0 + 7) / 8;
-        if (nt <= 1)
-            e = launch_nt<1>(p, sms, st);
-        else if (nt <= 2)
-            e = launch_nt<2>(p, sms, st);
-        else if (nt <= 4)
-            e = launch_nt<4>(p, sms, st);
-        else
-            e = launch_nt<8>(p, sms, st);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+    return r <= 8 ? launch_nt<1>(p, sms, st) : launch_nt<2>(p, sms, st);
 }
 
 }  // namespace qn
