@@ -124,10 +124,9 @@ __device__ __forceinline__ void load_js(const uint16_t *p, int count, bool vec, 
 // Everything comes straight into registers: with few tokens the factors are most of what is read, each once per 32 tokens.
 // The order of the features in a step is free as long as both operands agree, and so is the order of the columns j:
 //   x       lane t has the features 8 t .. 8 t + 7 of 32, two for each half of two MMAs; A's rows give the same pairs
-//   grad_h  lane t has the features 4 t .. 4 t + 3 of 16; of B it loads those rows, NT neighbouring j, and pairs rows by byte
-//           permutes
+//   grad_h  the same features; of B the lane loads those rows, NT neighbouring j, and pairs rows by byte permutes
 // Column g of the MMA's tile nt is j = NT g + nt.
-template <int NT, bool kX, bool kDrop>
+template <int NT, bool kX, bool kDrop, bool kAligned>
 __device__ __forceinline__ void down(const GradArgs &p, float *red, int j0, int64_t tile, uint32_t rank, uint32_t ranks) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int64_t m0 = tile * kDownTokens;
@@ -193,35 +192,28 @@ __device__ __forceinline__ void down(const GradArgs &p, float *red, int j0, int6
         } else {
 #pragma unroll
             for (int h = 0; h < 4; ++h) sc[h] = 1.0f;
-            const bool pairs = p.n % 4 == 0;
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-                const int64_t c0 = c * kPiece + 16 * ks + 4 * t;
-                uint2 v[4];
-                uint32_t w[4][(NT + 1) / 2];
+            for (int sub = 0; sub < 2; ++sub) {
+                const int64_t c0 = c * kPiece + 32 * sub + 8 * t;
+                uint4 v[4];
+                uint32_t w[8][(NT + 1) / 2];
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    const uint16_t *src = p.gh + row[h] * p.n + c0;
-                    v[h] = make_uint2(0u, 0u);
-                    if (pairs) {
-                        if (live[h] && c0 < p.n) v[h] = ld_ro_v2(src);
-                    } else if (live[h]) {
-                        uint32_t e[4];
+                for (int h = 0; h < 4; ++h)
+                    v[h] = live[h] ? load_gh<kAligned>(p.gh + row[h] * p.n, c0, p.n, p.gh + p.M * p.n) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) e[q] = c0 + q < p.n ? ld_ro_u16(src + q) : 0u;
-                        v[h] = make_uint2(e[0] | e[1] << 16, e[2] | e[3] << 16);
-                    }
-                }
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
+                for (int q = 0; q < 8; ++q)
                     load_js<NT>(p.B + (c0 + q) * p.r + j0 + NT * g, c0 + q < p.n ? js - NT * g : 0, vec, w[q]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const uint32_t sel = (nt & 1) ? 0x7632 : 0x5410;
-                    const uint32_t b0 = __byte_perm(w[0][nt / 2], w[1][nt / 2], sel), b1 = __byte_perm(w[2][nt / 2], w[3][nt / 2], sel);
+                    uint32_t b[4];
 #pragma unroll
-                    for (int mt = 0; mt < 2; ++mt)
-                        mma_16816(d[mt][nt], v[2 * mt].x, v[2 * mt + 1].x, v[2 * mt].y, v[2 * mt + 1].y, b0, b1);
+                    for (int q = 0; q < 4; ++q) b[q] = __byte_perm(w[2 * q][nt / 2], w[2 * q + 1][nt / 2], sel);
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt) {
+                        mma_16816(d[mt][nt], v[2 * mt].x, v[2 * mt + 1].x, v[2 * mt].y, v[2 * mt + 1].y, b[0], b[1]);
+                        mma_16816(d[mt][nt], v[2 * mt].z, v[2 * mt + 1].z, v[2 * mt].w, v[2 * mt + 1].w, b[2], b[3]);
+                    }
                 }
             }
         }
@@ -278,7 +270,7 @@ __device__ __forceinline__ void down(const GradArgs &p, float *red, int j0, int6
 }
 
 // grid (ranks * token tiles, 2, blocks of 8 NT columns j): y = 0 takes u from grad_h, y = 1 t from the codes.
-template <int NT, bool kDrop>
+template <int NT, bool kDrop, bool kAligned>
 __global__ void __launch_bounds__(kDownThreads) k_down(const GradArgs p) {
     extern __shared__ __align__(16) float red[];
     const uint32_t rank = cluster_rank(), ranks = cluster_size();
@@ -286,9 +278,9 @@ __global__ void __launch_bounds__(kDownThreads) k_down(const GradArgs p) {
     grid_dependents_launch();
     const int j0 = static_cast<int>(blockIdx.z) * 8 * NT;
     if (blockIdx.y == 0)
-        down<NT, false, false>(p, red, j0, tile, rank, ranks);
+        down<NT, false, false, kAligned>(p, red, j0, tile, rank, ranks);
     else
-        down<NT, true, kDrop>(p, red, j0, tile, rank, ranks);
+        down<NT, true, kDrop, true>(p, red, j0, tile, rank, ranks);
 }
 
 // -------------------------------------------------------------- products over tokens
@@ -509,7 +501,7 @@ cudaError_t launch_pass(const GradArgs &p, int sms, cudaStream_t st) {
     const int64_t js = (p.r + 8 * NT - 1) / (8 * NT);
     int ranks = split_ranks(2 * tok * js, 2 * sms, rounds);
     if (tok * ranks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    cudaError_t e = launch_clusters(k_down<NT, kDrop>, dim3(static_cast<unsigned>(tok * ranks), 2, static_cast<unsigned>(js)),
+    cudaError_t e = launch_clusters(k_down<NT, kDrop, kAligned>, dim3(static_cast<unsigned>(tok * ranks), 2, static_cast<unsigned>(js)),
                                     kDownThreads, static_cast<size_t>(kDownWarps) * kDownTokens * (8 * NT + 1) * 4, ranks, false, p, st);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (p.n + kOutCols - 1) / kOutCols + (p.k + kOutCols - 1) / kOutCols;
