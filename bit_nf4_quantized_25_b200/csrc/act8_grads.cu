@@ -19,8 +19,10 @@
 //            and two token streams, a cluster splits the tokens. The A operand wants neighbouring tokens of one
 //            column in a register: a lane loads 8 columns of 4 tokens and pairs them with byte permutes.
 //
-// Measured: 256 x 256, 8 tokens, rank 4 5.9 us, 4096 x 4096, 16 tokens, rank 16 10.9 us; the latency of two kernels, each
-// of loads, a few MMAs and sums across a cluster, bounds them.
+// CTAs split the rank too, in blocks of 8 or 16 columns j.
+//
+// Measured: 256 x 256, 8 tokens, rank 4 5.8 us, 4096 x 4096, 16 tokens, rank 16 8.0 us; the latency of two kernels, each
+// of loads, a few MMAs and sums across a cluster, bounds them. 28672 x 8192, 120 tokens, rank 64 39.6 us.
 #include "act8.cuh"
 #include "act8.h"
 #include "dropout.cuh"
@@ -541,7 +543,10 @@ cudaError_t launch_act8_grads(const int8_t *codes, const uint16_t *absmax, const
     if (e != cudaSuccess) return e;
     GradArgs p{codes, absmax, gh, M, n, k, A, B, r, s, grad_A, grad_B, static_cast<float *>(ws), nullptr, drop};
     p.u = p.t + (M + 15) / 16 * 16 * ((r + 7) / 8 * 8);
-    return r <= 8 ? launch_nt<1>(p, sms, st) : launch_nt<2>(p, sms, st);
+    // Blocks of 8 columns j as long as blocks of 16 would not fill the SMs twice: 4096 x 4096, 16 tokens, rank 16 8.0 us against
+    // 10.1; with more CTAs blocks of 16, which read x and grad_h half as often: 28672 x 8192, 120 tokens, rank 64 39.6 us against 49.1.
+    const int64_t tiles = (n + kOutCols - 1) / kOutCols + (k + kOutCols - 1) / kOutCols;
+    return tiles * ((r + 15) / 16) <= 2 * sms ? launch_nt<1>(p, sms, st) : launch_nt<2>(p, sms, st);
 }
 
 }  // namespace qn
