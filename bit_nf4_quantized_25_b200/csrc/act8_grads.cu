@@ -520,8 +520,13 @@ cudaError_t launch_nt(const GradArgs &p, int sms, cudaStream_t st) {
     return drop ? launch_pass<NT, true, false>(p, sms, st) : launch_pass<NT, false, false>(p, sms, st);
 }
 
-// Batches from this many tokens on go to the tcgen05 kernels.
-constexpr int64_t kTcTokens = 128;
+// Batches below 128 tokens, and below 1024 as long as the products are small, stay here; the others go to the tcgen05 kernels.
+// Measured here and there: 4096 x 4096, rank 16 128 tokens 10.5 and 15.2 us, 256 tokens 17.1 and 15.5; 1024 x 1024, rank 8,
+// 1024 tokens 11.2 and 15.8; 11008 x 4096, rank 64, 128 tokens 27.8 and 20.6.
+constexpr int64_t kFewTokens = 128, kFewTokensSmall = 1024, kSmall = 24 << 20;  // tokens x features x rank (in eights)
+bool few(int64_t M, int64_t n, int64_t k, int r) {
+    return M < kFewTokens || (M <= kFewTokensSmall && M * (n + k) <= kSmall / ((r + 7) / 8 * 8));
+}
 // Workspace of these kernels: t and u.
 size_t few_bytes(int64_t M, int r) {
     return 2 * sizeof(float) * static_cast<size_t>((M + 15) / 16) * 16 * static_cast<size_t>((r + 7) / 8 * 8);
@@ -530,13 +535,14 @@ size_t few_bytes(int64_t M, int r) {
 }  // namespace
 
 size_t act8_grads_workspace_bytes(int64_t M, int64_t n, int r) {
-    return M >= kTcTokens ? act8_grads_tc_workspace_bytes(M, n, r) : few_bytes(M, r);
+    const size_t here = few_bytes(M, r), there = act8_grads_tc_workspace_bytes(M, n, r);  // k decides, which is not known
+    return M < kFewTokens ? here : M > kFewTokensSmall || there > here ? there : here;
 }
 
 cudaError_t launch_act8_grads(const int8_t *codes, const uint16_t *absmax, const uint16_t *gh, int64_t M, int64_t n,
                               int64_t k, const uint16_t *A, const uint16_t *B, int r, float s, const DropoutArgs &drop,
                               float *grad_A, float *grad_B, void *ws, cudaStream_t st) {
-    if (M >= kTcTokens)
+    if (!few(M, n, k, r))
         return launch_act8_grads_tc(codes, absmax, gh, M, n, k, A, B, r, s, drop, grad_A, grad_B, ws, st);
     int sms = 148;
     cudaError_t e = device_sm_count(&sms);

@@ -364,7 +364,8 @@ qn_status act8_quantize(const void *x, const qn_act8 *out, void *stream);
 qn_status act8_dequantize(const qn_act8 *a, void *x_out, void *stream);
 
 /* Workspace bytes qlora_lora_grads_act8 needs for M tokens, n_out output features and
- * rank r (1..256); from 128 tokens on it holds a copy of grad_h where n_out % 8 != 0.
+ * rank r (1..256); from 128 tokens on there is room for a copy of grad_h where
+ * n_out % 8 != 0.
  * Host-only. The workspace's contents on entry do not matter. */
 qn_status qlora_lora_grads_act8_workspace_size(int64_t M, int64_t n_out, int r, size_t *ws_bytes);
 

@@ -257,6 +257,44 @@ def test_grads_long_batches(n, k, r):
     check_grads(*grad_inputs(4099, n, k, r, seed=n), 32.0)
 
 
+# from 1025 tokens on the kernels for long batches run whatever the rest is
+@pytest.mark.parametrize("M", [1024, 1025, 1056, 1087, 1151, 1152, 1153])
+def test_grads_long_batch_tokens(M):
+    check_grads(*grad_inputs(M, 200, 192, 16, seed=M), 32.0)
+
+
+@pytest.mark.parametrize("r", [1, 3, 8, 13, 16, 17, 32, 33, 64, 65, 100, 128, 256])
+def test_grads_long_batch_ranks(r):
+    check_grads(*grad_inputs(1070, 136, 320, r, seed=r), 2.0 * r)
+
+
+@pytest.mark.parametrize("n,k", [(1, 64), (7, 64), (8, 128), (63, 448), (255, 256), (257, 320), (1000, 64 * 21), (4097, 64 * 17)])
+def test_grads_long_batch_shapes(n, k):
+    check_grads(*grad_inputs(1150, n, k, 16, seed=n), 32.0)
+
+
+def test_grads_long_batch_dropout(oracle):
+    M, n, k, r = 1100, 200, 320, 24
+    p, seed, offset = 0.25, 1234567890123, 2 ** 33 + 1
+    keep = torch.from_numpy(oracle.dropout_keep(seed, offset, p, M, k)).to(DEV)
+    check_grads(*grad_inputs(M, n, k, r), 8.0, keep=keep.double(), dropout=(p, seed, offset))
+
+
+def test_grads_long_batch_is_reproducible_and_stays_inside_its_buffers():
+    M, n, k, r = 1130, 205, 192, 13
+    x8, gh, A, B = grad_inputs(M, n, k, r)
+    aw, a = guarded(r * k, torch.float32, 3.0)
+    bw, b = guarded(n * r, torch.float32, 5.0)
+    need = qb.lora_grads_act8_workspace_size(M, n, r)
+    ww = torch.full((need + 512,), 77, dtype=torch.uint8, device=DEV)
+    w = ww[256:256 + need]
+    first = check_grads(x8, gh, A, B, 8.0, grad_A=a.view(r, k), grad_B=b.view(n, r), workspace=w)
+    again = qb.qlora_lora_grads_act8(x8, gh, A, B, 8.0)
+    assert all(torch.equal(p, q) for p, q in zip(first, again))
+    assert guards_kept(aw, 3.0) and guards_kept(bw, 5.0)
+    assert bool((ww[:256] == 77).all()) and bool((ww[-256:] == 77).all())
+
+
 def test_grads_70b_layer():
     check_grads(*grad_inputs(1030, 28672, 8192, 64, seed=1), 16.0)
 
@@ -560,7 +598,7 @@ def test_calls_on_another_stream_and_in_a_graph():
         assert all(torch.equal(a, b) for a, b in zip(kept, step()))
 
 
-@pytest.mark.parametrize("M,n,k,r,dropout", [(200, 1001, 448, 70, None), (300, 512, 512, 16, (0.1, 5, 3)), (40, 130, 192, 90, None)])
+@pytest.mark.parametrize("M,n,k,r,dropout", [(1200, 1001, 448, 70, None), (1300, 512, 512, 16, (0.1, 5, 3)), (200, 1001, 448, 70, None), (40, 130, 192, 90, None)])
 def test_grads_in_a_graph(M, n, k, r, dropout):
     x8, gh, A, B = grad_inputs(M, n, k, r)
     ws = torch.empty(qb.lora_grads_act8_workspace_size(M, n, r), dtype=torch.uint8, device=DEV)
