@@ -1091,19 +1091,34 @@ cudaError_t launch_clusters(K kern, dim3 grid, int threads, size_t smem, int ran
     return e;
 }
 
-// rows x cols bf16 to rows of up8(cols), zeros behind: 8 values of a row per thread, cut out of the aligned words around them.
-__global__ void __launch_bounds__(256) k_pad(const uint16_t *src, int64_t rows, int64_t cols, int64_t chunks, uint16_t *to) {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, row = i / chunks, c = (i - row * chunks) * 8;
-    if (row >= rows) return;
-    *reinterpret_cast<uint4 *>(to + 8 * i) = act8::load_row8(src + row * cols, c, cols, src + rows * cols);
+// Copies of up to two matrices, rows x cols bf16 to rows of up8(cols), zeros behind: 8 values of a row per thread, cut out of
+// the aligned words around them. A CTA has `per_cta` rows, or a row has `ctas_row` CTAs.
+struct Pad {
+    const uint16_t *src;
+    int64_t rows, cols;
+    uint16_t *to;
+    unsigned chunks, per_cta, ctas_row, ctas;  // chunks: of 8 in a row
+};
+
+__global__ void __launch_bounds__(256) k_pad(const Pad a, const Pad b) {
+    const bool second = blockIdx.x >= a.ctas;
+    const Pad &p = second ? b : a;
+    const unsigned cta = second ? blockIdx.x - a.ctas : blockIdx.x;
+    const unsigned r = threadIdx.x / p.chunks;
+    const int64_t row = p.ctas_row > 1 ? cta / p.ctas_row : static_cast<int64_t>(cta) * p.per_cta + r;
+    const unsigned chunk = p.ctas_row > 1 ? cta % p.ctas_row * 256 + threadIdx.x : threadIdx.x - r * p.chunks;
+    if ((p.ctas_row == 1 && r >= p.per_cta) || row >= p.rows || chunk >= p.chunks) return;
+    const int64_t c = 8 * static_cast<int64_t>(chunk);
+    *reinterpret_cast<uint4 *>(p.to + row * 8 * p.chunks + c) = act8::load_row8(p.src + row * p.cols, c, p.cols, p.src + p.rows * p.cols);
 }
 
-cudaError_t launch_pad(const uint16_t *src, int64_t rows, int64_t cols, uint16_t *to, cudaStream_t st) {
-    const int64_t chunks = (cols + 7) / 8, ctas = (rows * chunks + 255) / 256;
-    if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    k_pad<<<static_cast<unsigned>(ctas), 256, 0, st>>>(src, rows, cols, chunks, to);
-    count_launch();
-    return cudaGetLastError();
+// False when it takes more CTAs than a grid holds.
+bool pad_of(const uint16_t *src, int64_t rows, int64_t cols, uint16_t *to, Pad *p) {
+    const int64_t chunks = (cols + 7) / 8, per_cta = chunks < 256 ? 256 / chunks : 1, ctas_row = (chunks + 255) / 256;
+    const int64_t ctas = ctas_row > 1 ? rows * ctas_row : (rows + per_cta - 1) / per_cta;
+    *p = {src, rows, cols, to, static_cast<unsigned>(chunks), static_cast<unsigned>(per_cta), static_cast<unsigned>(ctas_row),
+          static_cast<unsigned>(ctas)};
+    return ctas <= 0x3fffffffLL;
 }
 
 // Clusters of 1 .. 8 CTAs, one on an SM, that are resident at once: of the current context, kept per host thread.
@@ -1202,18 +1217,24 @@ cudaError_t launch_act8_grads_tc(const int8_t *codes, const uint16_t *absmax, co
     char *at = static_cast<char *>(ws) + mid_bytes(M, r);
     p.u = reinterpret_cast<uint16_t *>(at);
     at += mid_bytes(M, r);
+    Pad pads[2] = {};
+    int count = 0;
     if (n % 8) {
         uint16_t *to = reinterpret_cast<uint16_t *>(at);
         at += up256(2 * static_cast<size_t>(M) * static_cast<size_t>(up8(n)));
-        e = launch_pad(gh, M, n, to, st);
-        if (e != cudaSuccess) return e;
+        if (!pad_of(gh, M, n, to, &pads[count++])) return cudaErrorInvalidConfiguration;
         gh = to;
     }
     if (r % 8) {
         uint16_t *to = reinterpret_cast<uint16_t *>(at);
-        e = launch_pad(B, n, r, to, st);
-        if (e != cudaSuccess) return e;
+        if (!pad_of(B, n, r, to, &pads[count++])) return cudaErrorInvalidConfiguration;
         B = to;
+    }
+    if (count) {
+        k_pad<<<pads[0].ctas + pads[1].ctas, 256, 0, st>>>(pads[0], pads[1]);
+        count_launch();
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
     }
     CUtensorMap tm_gh, tm_codes, tm_A, tm_B, tm_t, tm_u;
     if (!make_map(&tm_gh, gh, M, up8(n), false) || !make_map(&tm_codes, codes, M, k, true) || !make_map(&tm_B, B, n, up8(r), false))
