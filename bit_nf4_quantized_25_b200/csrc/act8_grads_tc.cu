@@ -280,7 +280,8 @@ template <int kN, int kGroups, typename At, typename Put>
 __device__ __forceinline__ bool load_absmax(int steps, uint32_t afull, uint32_t aempty, int lane, At &&at, Put &&put) {
     Ring b;
     for (int i = 0; i < steps; i += kBatch, b.next(kBatches)) {
-        // all loads of whole, aligned groups before the first use, then the values of the others
+        // All loads before the first use. Rows of an odd number of blocks put groups on any 2-byte boundary: value by value then,
+        // those that do not exist from the group's first place (`at` points into the array even when none does).
         uint64_t v[kGroups / 32];
         bool rest = false;
 #pragma unroll
@@ -294,16 +295,21 @@ __device__ __forceinline__ bool load_absmax(int steps, uint32_t afull, uint32_t 
                 rest = true;
         }
         if (rest) {
+            uint32_t w[kGroups / 32][kN];
 #pragma unroll
             for (int g = 0; g < kGroups / 32; ++g) {
                 int count;
                 const uint16_t *p = at(i, 32 * g + lane, count);
-                if (count >= kN && (reinterpret_cast<uintptr_t>(p) & (2u * kN - 1u)) == 0) continue;
-                uint32_t w[kN];
 #pragma unroll
-                for (int e = 0; e < kN; ++e) w[e] = e < count ? ld_nc_u16(p + e) : 0u;
+                for (int e = 0; e < kN; ++e) w[g][e] = ld_nc_u16(p + (e < count ? e : 0));
+            }
 #pragma unroll
-                for (int e = 0; e < kN; ++e) v[g] |= static_cast<uint64_t>(w[e]) << (16 * e);
+            for (int g = 0; g < kGroups / 32; ++g) {
+                int count;
+                at(i, 32 * g + lane, count);
+                v[g] = 0;
+#pragma unroll
+                for (int e = 0; e < kN; ++e) v[g] |= static_cast<uint64_t>(e < count ? w[g][e] : 0u) << (16 * e);
             }
         }
         if (i >= kBatches * kBatch && !bar_wait(aempty + 8 * b.slot, b.phase ^ 1u)) return false;
