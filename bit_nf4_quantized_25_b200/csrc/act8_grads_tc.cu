@@ -23,7 +23,7 @@
 // Warp 0 issues the TMA loads, warp 1 the MMAs, one warp brings absmaxes, the others convert codes, drain accumulators and
 // run the epilogue. Every wait is bounded; a CTA whose wait runs out drains what it issued and its results are NaN.
 //
-// Measured at 4096 tokens: 4096 x 4096, rank 16 41 us (the bytes once: 8 us), 28672 x 8192, rank 64 132 us (44 us). A step
+// Measured at 4096 tokens: 4096 x 4096, rank 16 40 us (the bytes once: 8 us), 28672 x 8192, rank 64 128 us (44 us). A step
 // of k_outer_tc takes 0.42 us of x (conversion: ldmatrix, products and tcgen05.st of one step are a chain of 1.4 us, in
 // four groups) and of grad_h (32 KB); to that come 5 us until the first step of x and 5 us of epilogue.
 #include <cudaTypedefs.h>
@@ -1170,7 +1170,7 @@ int cluster_size(const Fits &fits, int per_sm, int64_t tiles, int64_t steps, int
 
 // Column tiles of the second kernel: the first `first` ones in clusters of c CTAs, the rest in clusters of c_rest in a launch of
 // their own, as the least waves x (steps + besides) in all want it (a launch costs `again` more). 112 + 64 tiles of 64 steps
-// (28672 x 8192, 4096 tokens) are three waves of clusters of 2, but one of 148 CTAs and one of 28 clusters.
+// (28672 x 8192, 4096 tokens) are three waves of clusters of 2, but one of 148 CTAs and one of 28 clusters: 149 us became 132.
 struct Split {
     int64_t first;
     int c, c_rest;

@@ -15,12 +15,12 @@
 // A cluster has a range of 16-row tiles, its CTAs (slices) split k. A CTA keeps its part of x, all of it, in shared
 // memory, so x is read from L2 once per CTA: all SMs ask for the same lines of it at about the same time, and with x from
 // L2 in the loop 8192 x 28672 at 16 tokens took 84 us (by plain loads; 107 us through a ring of asynchronous copies)
-// instead of 62. The 16 warps of a CTA take a tile each, and when fewer than 16 are left, split k for them once more. A
+// instead of 62, now 59. The 16 warps of a CTA take a tile each, and when fewer than 16 are left, split k for them once more. A
 // warp has kSlots steps of its weights in flight, in a ring of its own: asynchronous copies, since loads to registers
 // that are waited for one by one end up waiting for the youngest. The parts' sums meet in shared memory.
 //
-// Measured, with zero points: 4096 x 4096 (group 128) 1 token 6.7 us; 8192 x 28672 (128) 1, 8 and 16 tokens 34.7, 41.4 and
-// 58.8 us (3.5, 3.0 and 2.1 TB/s); 11008 x 4096 (32) 5 tokens 14.2 us. Three quarters of the warps' time goes by in the
+// Measured, with zero points: 4096 x 4096 (group 128) 1 token 6.7 us; 8192 x 28672 (128) 1, 8 and 16 tokens 34.5, 41.3 and
+// 59.1 us (3.6, 3.0 and 2.1 TB/s); 11008 x 4096 (32) 5 tokens 14.2 us. Three quarters of the warps' time goes by in the
 // loop, 190 instructions of a warp for 16 rows x 128 k at 16 tokens, and no pipe is busy for a third of it: waits between
 // dependent instructions bound it, four warps to a scheduler. x of 16 tokens leaves no room for more, and 120 of 148 SMs hold
 // the clusters of 8 that it needs. Small calls are start-up, the copy of x and the sums across CTAs.
