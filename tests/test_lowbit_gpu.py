@@ -3,6 +3,8 @@ forms (lowbit_ref).
 
 Tolerances. A bf16 result is off by half a step, 2^-8 of its value, from the rounding, plus what the fp32
 arithmetic before it is off; that part is derived at each test. Codes are compared for equality."""
+import threading
+
 import pytest
 import torch
 
@@ -639,6 +641,32 @@ def test_calls_side_by_side_on_two_streams():
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(a, b) for g in got[i] for a, b in zip(g, want[i]))
+
+
+def test_host_threads_with_a_stream_each():
+    x8, gh, A, B = grad_inputs(1100, 512, 512, 16)
+    w, x = random_int4(4096, 4096, 64, True, seed=1), rand(16, 4096, seed=2)
+
+    def run():
+        return (qb.int4_linear_fwd(w, x), *qb.qlora_lora_grads_act8(x8, gh, A, B, 8.0), qb.act8_quantize(x).codes)
+
+    want = run()
+    torch.cuda.synchronize()
+    same = []
+
+    def work():
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            got = [run() for _ in range(20)]
+        side.synchronize()
+        same.append(all(torch.equal(p, q) for g in got for p, q in zip(g, want)))
+
+    threads = [threading.Thread(target=work) for _ in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert same == [True] * 3
 
 
 @pytest.mark.parametrize("rows,cols", [(3, 192), (700, 4096)])
