@@ -6,6 +6,7 @@
 //   symmetric:        s = bf16(fl32(max |w| / 7)), z = 8
 //   q = clamp(round(w / s) + z, 0, 15), rounding to nearest with halves away from zero; a group whose s is
 //   0 has q = z.
+//   A group with a NaN or an infinity has s = NaN, z = 0 (8 without zero points) and q = z: it reads back NaN.
 //
 // Both directions are bound by HBM: 2 B and 0.5 B + 2 or 3 B per group for each weight. A lane takes 8
 // weights (one 16-byte word of W, one 4-byte word of codes); a group is 4, 8 or 16 neighbouring lanes,
@@ -26,13 +27,13 @@ constexpr int kThreads = 256;
 constexpr int kUnroll = 4;
 constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it leaves an integer in the low mantissa bits
 
-__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {  // of bf16 pairs
-    const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {  // of bf16 pairs; NaN where either is
+    const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
     return *reinterpret_cast<const uint32_t *>(&m);
 }
 
-// A group's largest weight and the size of its smallest, both at least 0, or (not kZero) its largest size; all lanes of the
-// warp call it. Both run through one bf16 pair: (max w, max -w).
+// A group's largest weight and the size of its smallest, both at least 0, or (not kZero) its largest size; NaN (both, or the
+// one) when the group holds a NaN. All lanes of the warp call it. Both run through one bf16 pair: (max w, max -w).
 template <int kGroup, bool kZero>
 __device__ __forceinline__ void range(const uint4 &v, float &hi, float &below) {
     constexpr uint32_t kSigns = 0x80008000u;
@@ -47,9 +48,9 @@ __device__ __forceinline__ void range(const uint4 &v, float &hi, float &below) {
 #pragma unroll
     for (int d = 1; d < kGroup / 8; d <<= 1) m = max2(m, __shfl_xor_sync(0xffffffffu, m, d));
     m = max2(m, 0u);
+    if (!kZero) m = max(m & 0xffffu, m >> 16);  // as integers, which puts a NaN above all: the bits have no sign
     hi = bf16_lo(m);
     below = bf16_hi(m);
-    if (!kZero) hi = fmaxf(hi, below);
 }
 
 // Scale, zero point and codes of a lane's 8 weights in a group with this range.
@@ -61,6 +62,7 @@ __device__ __forceinline__ void range(const uint4 &v, float &hi, float &below) {
 template <bool kZero>
 __device__ __noinline__ uint4 encode_any(uint4 v, float hi, float below) {  // codes, scale, zero point
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    if (!(hi <= 3.4028235e38f && below <= 3.4028235e38f)) return make_uint4(kZero ? 0u : 0x88888888u, 0x7fc0u, kZero ? 0u : 8u, 0u);
     float span = kZero ? hi + below : hi;
     if (kZero && span > 3.4028235e38f) span = 2.0f * __fdiv_rn(0.5f * hi + 0.5f * below, 15.0f);  // hi + below overflowed
     else span = __fdiv_rn(span, kZero ? 15.0f : 7.0f);

@@ -416,7 +416,7 @@ qn_status swiglu_act8_bwd(const qn_act8 *gate8, const qn_act8 *up8, const void *
  * served from. No counterpart on the pages.
  *
  * A group is `group` = 32, 64 or 128 consecutive weights of a row; a weight is
- * s * (q - z) with the group's bf16 scale s >= 0, its zero point z in 0..15 and the
+ * s * (q - z) with the group's bf16 scale s >= 0 (or NaN), its zero point z in 0..15 and the
  * code q in 0..15.
  *   n_out, k_in : k_in % group == 0 and k_in % 64 == 0
  *   codes       : n_out*k_in/2 bytes, row-major, the element order of qn_nf4_weight
@@ -440,11 +440,13 @@ typedef struct {
 qn_status qn_int4_sizes(int64_t n_out, int64_t k_in, int group, size_t *codes_bytes, size_t *scale_bytes,
                         size_t *zero_bytes);
 
-/* int4_quantize -- W (n_out x k_in bf16, finite) -> out, with round = to nearest, halves
+/* int4_quantize -- W (n_out x k_in bf16) -> out, with round = to nearest, halves
  * away from zero. With out->zero_point: lo = min(0, min w), hi = max(0, max w),
  * s = bf16_rn(fl32((hi - lo) / 15)), z = clamp(round(-lo / s), 0, 15). Without:
  * s = bf16_rn(fl32(max |w| / 7)), z = 8. q = clamp(round(w / s) + z, 0, 15). A group
- * whose s is 0 has z = 0 (8 without zero points) and q = z.
+ * whose s is 0 has z = 0 (8 without zero points) and q = z. A group that holds a NaN or an
+ * infinity has s = NaN, z as with s = 0 and q = z: all its weights read back as NaN, and a
+ * product with its row is NaN.
  * Errors: QN_EINVAL, QN_ESHAPE, QN_EALIGN (W or codes not 16-byte aligned, scale not
  * 2-byte aligned), QN_ECUDA. */
 qn_status int4_quantize(const void *W, const qn_int4_weight *out, void *stream);
