@@ -50,9 +50,24 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                       pack_bf16x2(f[6], f[7]));
 }
 
-// The hardware exponential and reciprocal: a few units in the last place of fp32, far below the bf16
-// rounding of the results. exp(-g) = inf gives sigma = 0.
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+__device__ __forceinline__ float reciprocal(float v) {  // of 1 .. 2^126, by the hardware's
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// sigma(g) = e / (1 + e) below 0 and 1 / (1 + e) from 0 on, with e = exp(-|g|) <= 1, so that no gate leads out of the
+// reciprocal's range. By the hardware exponential, of a rounded argument, and reciprocal it is off by at most
+// (3 + 1.2 |g|) 2^-23 of itself, below 2^-16 in all of fp32's normal range and far below the bf16 rounding of the results;
+// below 2^-126 it is a multiple of 2^-149.
+__device__ __forceinline__ float sigmoid(float g) {
+    const float e = __expf(-fabsf(g));
+    return (g < 0.0f ? e : 1.0f) * reciprocal(1.0f + e);
+}
+
+// The same for |g| up to about kNear, three instructions less.
+constexpr uint32_t kNear = 0x42aeu;  // 87 in bf16: exp(87.3) is 2^126
+__device__ __forceinline__ float sigmoid_near(float g) { return reciprocal(1.0f + __expf(-g)); }
 
 template <int kUnroll>
 __global__ void __launch_bounds__(kThreads) k_act8_quantize(const uint16_t *x, int64_t words, int8_t *codes,
@@ -153,9 +168,19 @@ __global__ void __launch_bounds__(kThreads) k_swiglu_act8_bwd(const int8_t *gq, 
         decode8(g[u], act8::step(gt[u]), a);
         decode8(w[u], act8::step(ut[u]), b);
         unpack8(d[u], dy);
+        // Issuing instructions bounds the kernel, so blocks of ordinary gates do without sigmoid's other half: at
+        // 4096 x 11008 72.7 us against 75.1.
+        float sg[8];
+        if (gt[u] <= kNear) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sg[e] = sigmoid_near(a[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sg[e] = sigmoid(a[e]);
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float sig = sigmoid(a[e]), sl = a[e] * sig;
+            const float sig = sg[e], sl = a[e] * sig;
             dg[e] = dy[e] * b[e] * sig * (1.0f + a[e] * (1.0f - sig));
             du[e] = dy[e] * sl;
             f[e] = sl * b[e];

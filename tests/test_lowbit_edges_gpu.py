@@ -1,5 +1,5 @@
 """The 8-bit activations and the 4-bit integer weights on the GPU where their other tests do not reach: weights that are not
-finite. Compared with 64-bit forms (lowbit_ref)."""
+finite, gates far below zero. Compared with 64-bit forms (lowbit_ref)."""
 import pytest
 import torch
 
@@ -10,7 +10,7 @@ if not torch.cuda.is_available():
 
 import lowbit_ref as ref
 from bit_nf4_quantized_25_b200 import binding as qb
-from test_lowbit_gpu import DEV, rand
+from test_lowbit_gpu import BF, DEV, TINY, rand, within
 
 
 # ------------------------------------------------------------------- 4-bit integers
@@ -44,3 +44,38 @@ def test_int4_a_weight_that_is_not_finite_marks_its_group_and_no_other(bad, grou
     x = rand(3, k, seed=1)
     h, h0 = qb.int4_linear_fwd(w, x), qb.int4_linear_fwd(clean, x)
     assert bool(h[:, 1:].isnan().all()) and torch.equal(h[:, 0], h0[:, 0])
+
+
+# ---------------------------------------------------------------------------- SwiGLU
+
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** 40])
+def test_swiglu_of_gates_far_below_zero(scale):
+    # exp(-g) leaves fp32 on the way down: the results do not, by far, where up is large or g is above -104
+    gate = torch.linspace(-103.0, -84.0, 64 * 32, device=DEV).to(BF).reshape(4, -1)
+    up, dy = (rand(4, 512, seed=1).float() * scale).to(BF), rand(4, 512, seed=2)
+    y, g8, u8 = qb.swiglu_act8_fwd(gate, up)
+    # exp of a rounded argument and the products as in the other tests; below 2^-126 sigma is a multiple of 2^-149, and
+    # exp, the quotient and two products may each be off by one
+    def few(g, *factors):
+        f = 1.0 + g.abs()
+        for t in factors:
+            f = f * (1.0 + t.abs())
+        return f * 4.0 * 2.0 ** -149
+
+    g, u = gate.double(), up.double()
+    eta = (6.0 + 1.2 * g.abs()) * 2.0 ** -23
+    want = ref.swiglu(g, u)
+    assert float(want.abs().max()) > 2.0 ** -118 and int((want.abs() > 2.0 ** -126).sum()) > 500
+    within(y, want, want.abs() * (ref.HALF_STEP + 1.01 * eta) + few(g, u) + TINY, "y")
+
+    gg, gu, y8 = qb.swiglu_act8_bwd(g8, u8, dy)
+    g, u, d = ref.act8_values(g8.codes, g8.absmax), ref.act8_values(u8.codes, u8.absmax), dy.double()
+    eta = (8.0 + 1.2 * g.abs()) * 2.0 ** -23
+    dg, du = ref.swiglu_grads(g, u, d)
+    # 1 + g (1 - sigma) is near g here and does not cancel: two roundings
+    within(gg, dg, dg.abs() * (ref.HALF_STEP + 1.01 * eta + 2.0 ** -22) + few(g, u, d) + TINY, "grad_gate")
+    within(gu, du, du.abs() * (ref.HALF_STEP + 1.01 * eta) + few(g, d) + TINY, "grad_up")
+    want = ref.swiglu(g, u)
+    top = want.abs().reshape(4, -1, 64).amax(-1, keepdim=True).expand(-1, -1, 64).reshape(want.shape)
+    rounding = top * (ref.HALF_STEP + 1.01 * eta) + few(g, u) + TINY
+    within(ref.act8_values(y8.codes, y8.absmax), want, rounding + top * 1.02 / 254.0, "y8")
