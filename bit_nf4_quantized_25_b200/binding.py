@@ -30,7 +30,7 @@ EXPORTED = ("qn_nf4_sizes", "qn_weight_sizes", "qn_quantize_workspace_size", "nf
             "act8_dequantize", "qlora_lora_grads_act8_workspace_size", "qlora_lora_grads_act8", "swiglu_act8_fwd",
             "swiglu_act8_bwd", "qn_int4_sizes", "int4_quantize", "int4_dequantize", "int4_linear_fwd",
             "qn_status_string",
-            "qn_last_error", "qn_launch_count", "qn_selftest_wait_timeout")
+            "qn_last_error", "qn_launch_count", "qn_selftest_wait_timeout", "qn_selftest_grads_give_up")
 
 
 class QNError(RuntimeError):
@@ -120,7 +120,8 @@ def load(path: str | None = None):
         lib.int4_quantize.argtypes = [P, I4, P]
         lib.int4_dequantize.argtypes = [I4, P, P]
         lib.int4_linear_fwd.argtypes = [I4, P, i64, P, P]
-        for f in ("qlora_lora_grads_act8_workspace_size", "qlora_lora_grads_act8", "qn_act8_sizes", "act8_quantize",
+        lib.qn_selftest_grads_give_up.argtypes = lib.qlora_lora_grads_act8.argtypes
+        for f in ("qlora_lora_grads_act8_workspace_size", "qlora_lora_grads_act8", "qn_selftest_grads_give_up", "qn_act8_sizes", "act8_quantize",
                   "act8_dequantize", "swiglu_act8_fwd", "swiglu_act8_bwd", "qn_int4_sizes", "int4_quantize",
                   "int4_dequantize", "int4_linear_fwd"):
             getattr(lib, f).restype = st
@@ -628,6 +629,18 @@ def qlora_lora_grads_act8(x: Act8, grad_h: torch.Tensor, A: torch.Tensor, B: tor
         r = _native().lora_grads(x.rows, x.cols, x.codes, x.absmax, grad_h, A, B, float(alpha))
         if r is not None:
             return _done(r, "qlora_lora_grads_act8")
+    return _grads_act8(load().qlora_lora_grads_act8, "qlora_lora_grads_act8", x, grad_h, A, B, alpha, grad_A, grad_B,
+                       workspace, stream, dropout)
+
+
+def selftest_grads_give_up(x: Act8, grad_h: torch.Tensor, A: torch.Tensor, B: torch.Tensor, alpha: float, dropout,
+                           stream=None):
+    """qlora_lora_grads_act8 in which waits run out (see qn_selftest_grads_give_up in the header): grad_A is NaN."""
+    return _grads_act8(load().qn_selftest_grads_give_up, "qn_selftest_grads_give_up", x, grad_h, A, B, alpha, None, None,
+                       None, stream, dropout)
+
+
+def _grads_act8(call, what: str, x, grad_h, A, B, alpha, grad_A, grad_B, workspace, stream, dropout):
     M, k = x.rows, x.cols
     n = _matrix(grad_h, "grad_h")[1]
     r = _matrix(A, "A")[0]
@@ -651,9 +664,8 @@ def qlora_lora_grads_act8(x: Act8, grad_h: torch.Tensor, A: torch.Tensor, B: tor
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
     d = None if dropout is None else ctypes.byref(_dropout_struct(dropout))
-    _check(load().qlora_lora_grads_act8(ctypes.byref(cx), grad_h.data_ptr(), n, A.data_ptr(), B.data_ptr(), r,
-                                        float(alpha), d, grad_A.data_ptr(), grad_B.data_ptr(), workspace.data_ptr(),
-                                        workspace.numel() * workspace.element_size(), s), "qlora_lora_grads_act8")
+    _check(call(ctypes.byref(cx), grad_h.data_ptr(), n, A.data_ptr(), B.data_ptr(), r, float(alpha), d, grad_A.data_ptr(),
+                grad_B.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), s), what)
     return grad_A, grad_B
 
 

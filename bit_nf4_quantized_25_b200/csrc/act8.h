@@ -32,10 +32,11 @@ cudaError_t launch_act8_grads(const int8_t *codes, const uint16_t *absmax, const
                               float *grad_A, float *grad_B, void *ws, cudaStream_t st);
 
 // The same on the 5th-generation tensor cores, for long batches. The workspace also holds copies of grad_h and B with
-// padded rows where TMA cannot read theirs (n % 8, r % 8).
+// padded rows where TMA cannot read theirs (n % 8, r % 8). give_up (with a dropout): waits of the second kernel run out.
 size_t act8_grads_tc_workspace_bytes(int64_t M, int64_t n, int r);
 cudaError_t launch_act8_grads_tc(const int8_t *codes, const uint16_t *absmax, const uint16_t *gh, int64_t M, int64_t n,
                                  int64_t k, const uint16_t *A, const uint16_t *B, int r, float s,
-                                 const DropoutArgs &drop, float *grad_A, float *grad_B, void *ws, cudaStream_t st);
+                                 const DropoutArgs &drop, float *grad_A, float *grad_B, void *ws, cudaStream_t st,
+                                 bool give_up = false);
 
 }  // namespace qn

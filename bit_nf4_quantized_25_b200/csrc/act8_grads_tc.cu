@@ -21,7 +21,9 @@
 //               what the first kernel read last is still in L2.
 //
 // Warp 0 issues the TMA loads, warp 1 the MMAs, one warp brings absmaxes, the others convert codes, drain accumulators and
-// run the epilogue. Every wait is bounded; a CTA whose wait runs out drains what it issued and its results are NaN.
+// run the epilogue. Every wait on an mbarrier is bounded; a CTA whose wait runs out drains what it issued and its results are
+// NaN. A warp gives up as a whole, since what follows a wait wants all its lanes, and the warps of a group that meet at
+// a barrier in every step leave together (see group_all).
 //
 // Measured at 4096 tokens: 4096 x 4096, rank 16 40 us (the bytes once: 8 us), 28672 x 8192, rank 64 128 us (44 us). A step
 // of k_outer_tc takes 0.42 us of x (conversion: ldmatrix, products and tcgen05.st of one step are a chain of 1.4 us, in
@@ -177,8 +179,10 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
     asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes) : "memory");
 }
 // Bounded, as sm100::mbar_wait.
+constexpr uint32_t kPolls = 1u << 24;
+template <uint32_t kLimit = kPolls>
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
-    for (uint32_t i = 0; i < (1u << 24); ++i) {
+    for (uint32_t i = 0; i < kLimit; ++i) {
         uint32_t ok;
         asm volatile(
             "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
@@ -188,6 +192,20 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
         if (ok) return true;
     }
     return false;
+}
+// One decision for the warp, whose lanes all call it and come out together: a wait that runs out in one lane may still have
+// ended in another.
+__device__ __forceinline__ bool warp_all(bool ok) { return __all_sync(0xffffffffu, ok); }
+// One decision for four warps, 128 threads, at the named barrier `id`, which orders their memory accesses as __syncthreads does.
+// A warp that has given up comes too; the named barrier itself has no limit.
+__device__ __forceinline__ bool group_all(uint32_t id, bool ok) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbar.red.and.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"(id), "r"(static_cast<uint32_t>(ok))
+        : "memory");
+    return all != 0;
 }
 // Whether the phase is over; does not wait.
 __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
@@ -276,7 +294,7 @@ constexpr int kBatch = 4, kBatches = 3;
 
 __device__ __forceinline__ uint64_t pair(uint2 v) { return static_cast<uint64_t>(v.y) << 32 | v.x; }
 
-template <int kN, int kGroups, typename At, typename Put>
+template <int kN, int kGroups, uint32_t kLimit, typename At, typename Put>
 __device__ __forceinline__ bool load_absmax(int steps, uint32_t afull, uint32_t aempty, int lane, At &&at, Put &&put) {
     Ring b;
     for (int i = 0; i < steps; i += kBatch, b.next(kBatches)) {
@@ -312,7 +330,7 @@ __device__ __forceinline__ bool load_absmax(int steps, uint32_t afull, uint32_t 
                 for (int e = 0; e < kN; ++e) v[g] |= static_cast<uint64_t>(e < count ? w[g][e] : 0u) << (16 * e);
             }
         }
-        if (i >= kBatches * kBatch && !bar_wait(aempty + 8 * b.slot, b.phase ^ 1u)) return false;
+        if (i >= kBatches * kBatch && !warp_all(bar_wait<kLimit>(aempty + 8 * b.slot, b.phase ^ 1u))) return false;
 #pragma unroll
         for (int g = 0; g < kGroups / 32; ++g) put(b.slot, 32 * g + lane, v[g]);
         __syncwarp();
@@ -469,9 +487,8 @@ __device__ __forceinline__ void down_tc(const CUtensorMap *act, const CUtensorMa
         int i = 0;
         Ring r, q;  // stages; grad_h: accumulators
         for (; i < steps; ++i, r.next(kStages)) {
-            if (!bar_wait(full + 8 * r.slot, r.phase)) break;
-            if (!kX && i % kSegment == 0 && i >= 4 * kSegment && !bar_wait(cempty + 8 * q.slot, q.phase ^ 1u)) break;
-            __syncwarp();
+            if (!warp_all(bar_wait(full + 8 * r.slot, r.phase))) break;
+            if (!kX && i % kSegment == 0 && i >= 4 * kSegment && !warp_all(bar_wait(cempty + 8 * q.slot, q.phase ^ 1u))) break;
             tc_fence_after();
             const uint64_t a = a0 + r.slot * (stage / 16), b = b0 + r.slot * (stage / 16);
             const uint32_t d = tmem + static_cast<uint32_t>(kX ? r.slot : q.slot) * p.rp;
@@ -494,7 +511,7 @@ __device__ __forceinline__ void down_tc(const CUtensorMap *act, const CUtensorMa
     } else if (kX && warp == kDownThreads / 32 - 1) {
         const int64_t blocks = p.k / kBlock;
         // a group: the batch's four steps of a token
-        if (!load_absmax<4, kDownTile>(
+        if (!load_absmax<4, kDownTile, kPolls>(
                 steps, afull, aempty, lane,
                 [&](int i, int row, int &count) {
                     const int64_t m = tok0 + static_cast<int64_t>(row);
@@ -517,7 +534,7 @@ __device__ __forceinline__ void down_tc(const CUtensorMap *act, const CUtensorMa
         for (int i = group; ok && i < steps + kStages; i += 2) {
             const int e = i - kStages, q = e & (kBatch - 1);
             if (e >= 0) {
-                ok = (q > 1 || bar_wait(afull + 8 * b.slot, b.phase)) && bar_wait(empty + 8 * r.slot, r.phase ^ 1u);
+                ok = warp_all((q > 1 || bar_wait(afull + 8 * b.slot, b.phase)) && bar_wait(empty + 8 * r.slot, r.phase ^ 1u));
                 if (!ok) break;
                 tc_fence_after();
                 add(static_cast<uint32_t>(r.slot * p.rp),
@@ -530,7 +547,7 @@ __device__ __forceinline__ void down_tc(const CUtensorMap *act, const CUtensorMa
                 }
             }
             if (i < steps) {
-                ok = bar_wait(cfull + 8 * c.slot, c.phase);
+                ok = warp_all(bar_wait(cfull + 8 * c.slot, c.phase));
                 if (!ok) break;
                 convert_block<kDrop>(codes + c.slot * (kDownA / 2) + row * 64u, row, p.drop,
                                      p.drop.offset + static_cast<uint64_t>(m * p.k + (lo + i) * kK),
@@ -552,7 +569,7 @@ __device__ __forceinline__ void down_tc(const CUtensorMap *act, const CUtensorMa
         Ring q;
         if (group == 1) q.next(4);
         for (int i = group * kSegment; i < steps; i += 2 * kSegment) {
-            if (!bar_wait(cfull + 8 * q.slot, q.phase)) {
+            if (!warp_all(bar_wait(cfull + 8 * q.slot, q.phase))) {
                 *abort_flag = 1u;
                 break;
             }
@@ -667,11 +684,13 @@ constexpr int kOutRowGh = 68;         // floats per column of grad_h of its sums
 static_assert(kColsGh * kOutRowGh * 4 <= kOutRoom && kOutSums % 16 == 0, "");
 constexpr size_t kOutSmem = 1024 + kOutRoom + kOutAbsmax + 512;
 
-template <bool kX, bool kDrop>
+// kGiveUp: a check of what happens when waits run out. From the middle of its steps on one warp of each group gives up, and
+// the other waits that this leaves without an end have a short limit.
+template <bool kX, bool kDrop, bool kGiveUp>
 __device__ __forceinline__ void outer_tc(const CUtensorMap *act, const CUtensorMap *mid, const TcArgs &p, uint8_t *smem,
                                          uint64_t *bars, int64_t tile, uint32_t rank, uint32_t ranks) {
     constexpr int kCols = kX ? kColsX : kColsGh;
-    constexpr uint32_t kAct = kX ? kOutCodes : kOutA;
+    constexpr uint32_t kAct = kX ? kOutCodes : kOutA, kLimit = kGiveUp ? 1u << 12 : kPolls;
     // Steps between two drains of the accumulators: the tensor core cuts off what it adds instead of rounding it, and a
     // chain of 256 MMAs would be off by 1e-5. Up to rank 32 there is TMEM for two accumulators in turn, which the MMAs do
     // not wait for, so drains are twice as frequent.
@@ -741,7 +760,7 @@ __device__ __forceinline__ void outer_tc(const CUtensorMap *act, const CUtensorM
     const int lane_x = (lane & 16) + ((lane & 7) << 1) + ((lane >> 3) & 1);
     Ring turn;
     auto drain = [&](bool first) -> bool {
-        if (!bar_wait(done + 8 * turn.slot, turn.phase)) return false;
+        if (!warp_all(!*abort_flag && bar_wait<kLimit>(done + 8 * turn.slot, turn.phase))) return false;
         tc_fence_after();
         const uint32_t d = tmem + 256 * h + 128 * turn.slot + ((quarter * 32u) << 16);
 #pragma unroll
@@ -794,7 +813,7 @@ __device__ __forceinline__ void outer_tc(const CUtensorMap *act, const CUtensorM
             grid_dependency_wait();
             while (i < steps && !*abort_flag) {
                 if (i >= issued) {
-                    if (!bar_wait(empty + 8 * ai.slot, ai.phase ^ 1u)) {
+                    if (!bar_wait<kLimit>(empty + 8 * ai.slot, ai.phase ^ 1u)) {
                         *abort_flag = 1u;
                         break;
                     }
@@ -818,15 +837,14 @@ __device__ __forceinline__ void outer_tc(const CUtensorMap *act, const CUtensorM
         while (ok && i < steps) {
             const int end = steps - i < every ? steps : i + every;
             if (i >= turns * every) {
-                ok = bar_wait(drained + 8 * d.slot, d.phase ^ 1u);
+                ok = warp_all(bar_wait<kLimit>(drained + 8 * d.slot, d.phase ^ 1u));
                 if (!ok) break;
             }
             const uint32_t acc = tmem + 128 * d.slot;
             uint32_t more = 0u;
             for (; i < end; ++i) {
-                ok = kX ? bar_wait(ready + 8 * t.slot, t.phase) : bar_wait(full + 8 * r.slot, r.phase);
+                ok = warp_all(kX ? bar_wait<kLimit>(ready + 8 * t.slot, t.phase) : bar_wait<kLimit>(full + 8 * r.slot, r.phase));
                 if (!ok) break;
-                __syncwarp();
                 tc_fence_after();
                 if (leader) {
 #pragma unroll
@@ -864,7 +882,7 @@ __device__ __forceinline__ void outer_tc(const CUtensorMap *act, const CUtensorM
     } else if (warp == 2 + kOutWarps) {
         const int64_t blocks = p.k / kBlock, blk0 = col0 / kBlock;
         // a group: a token's two blocks at one of the batch's four steps; kept as [step][block][token]
-        if (kX && !load_absmax<2, kBatch * kK>(
+        if (kX && !load_absmax<2, kBatch * kK, kLimit>(
                       steps, afull, aempty, lane,
                       [&](int i, int e, int &count) {
                           const int64_t m = tok(i + e / kK) + static_cast<int64_t>(e % kK);
@@ -880,7 +898,7 @@ __device__ __forceinline__ void outer_tc(const CUtensorMap *act, const CUtensorM
             *abort_flag = 1u;
     } else if (!kX || warp > 2 + kOutWarps) {
         for (int i = 0; i < steps && (kX || warp < 2 + kOutWarps); i += every)
-            if (*abort_flag || !drain(i == 0)) {
+            if (!drain(i == 0)) {
                 *abort_flag = 1u;
                 break;
             }
@@ -899,14 +917,16 @@ __device__ __forceinline__ void outer_tc(const CUtensorMap *act, const CUtensorM
         Ring last = r;  // the stage of the group's step before
         bool ok = true;
         for (int i = group; i < steps; i += 4) {
-            ok = bar_wait(afull + 8 * b.slot, b.phase) && bar_wait(full + 8 * r.slot, r.phase) && (i < 4 || bar_wait(empty + 8 * last.slot, last.phase));
-            if (!ok) break;
-            __syncwarp();
+            ok = ok && bar_wait<kLimit>(afull + 8 * b.slot, b.phase) && bar_wait<kLimit>(full + 8 * r.slot, r.phase) &&
+                 (i < 4 || bar_wait<kLimit>(empty + 8 * last.slot, last.phase));
+            if (kGiveUp && quarter == 0 && 2 * i >= steps) ok = false;
+            ok = warp_all(ok);
+            if (!kDrop && !ok) break;
             tc_fence_after();
             const uint32_t here = from + r.slot * stage;
             if (kDrop) {  // the step's codes, half a row of a block (32) a thread and turn, masked in place
 #pragma unroll 1
-                for (uint32_t e = quarter * 32u + lane; e < 256; e += 128) {
+                for (uint32_t e = quarter * 32u + lane; ok && e < 256; e += 128) {
                     const uint32_t token = e & 63u, part = e >> 6;
                     const uint32_t at = base + r.slot * stage + (part >> 1) * (kOutCodes / 2) + token * 64u;
                     const uint64_t e0 = p.drop.offset + static_cast<uint64_t>((tok(i) + static_cast<int64_t>(token)) * p.k + col0 + 32 * part);
@@ -922,7 +942,9 @@ __device__ __forceinline__ void outer_tc(const CUtensorMap *act, const CUtensorM
                     }
                 }
                 fence_proxy_async_smem();  // the stage's next load overwrites what was stored here
-                asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
+                __syncwarp();
+                ok = group_all(1u + static_cast<uint32_t>(group), ok);
+                if (!ok) break;
             }
             const uint16_t *am = absmax + ((b.slot * kBatch + group) * 2 + blk) * kK + 2 * (lane & 3);
 #pragma unroll
@@ -953,10 +975,10 @@ __device__ __forceinline__ void outer_tc(const CUtensorMap *act, const CUtensorM
             }
             tmem_st_wait();
             tc_fence_before();
-            ok = bar_wait(ufull + 8 * r.slot, r.phase);  // for the MMA thread, which then waits once
-            if (!ok) break;
+            ok = warp_all(bar_wait<kLimit>(ufull + 8 * r.slot, r.phase));  // for the MMA thread, which then waits once
+            if (!kDrop && !ok) break;  // with kDrop the other warps have to hear of it, at the next step's barrier
             __syncwarp();
-            if (lane == 0) {
+            if (ok && lane == 0) {
                 bar_arrive(ready + 8 * group);
                 bar_arrive(aempty + 8 * b.slot);
             }
@@ -1030,7 +1052,7 @@ __device__ __forceinline__ void outer_tc(const CUtensorMap *act, const CUtensorM
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-template <bool kDrop>
+template <bool kDrop, bool kGiveUp>
 __global__ void __launch_bounds__(kOutThreads, 1)
 k_outer_tc(const __grid_constant__ CUtensorMap tm_gh, const __grid_constant__ CUtensorMap tm_codes,
            const __grid_constant__ CUtensorMap tm_t, const __grid_constant__ CUtensorMap tm_u, const TcArgs p) {
@@ -1041,9 +1063,9 @@ k_outer_tc(const __grid_constant__ CUtensorMap tm_gh, const __grid_constant__ CU
     const int64_t tile = p.tile0 + blockIdx.x / ranks;
     const int64_t of_codes = tile - (p.codes_first ? 0 : (p.n + kColsGh - 1) / kColsGh), tiles_x = (p.k + kColsX - 1) / kColsX;
     if (of_codes >= 0 && of_codes < tiles_x)
-        outer_tc<true, kDrop>(&tm_codes, &tm_u, p, smem, bars, of_codes, rank, ranks);
+        outer_tc<true, kDrop, kGiveUp>(&tm_codes, &tm_u, p, smem, bars, of_codes, rank, ranks);
     else
-        outer_tc<false, false>(&tm_gh, &tm_t, p, smem, bars, p.codes_first ? tile - tiles_x : tile, rank, ranks);
+        outer_tc<false, false, false>(&tm_gh, &tm_t, p, smem, bars, p.codes_first ? tile - tiles_x : tile, rank, ranks);
 }
 
 // ------------------------------------------------------------------------------------ host
@@ -1142,7 +1164,7 @@ cudaError_t cluster_fits(const Fits **out) {
     const uint64_t ctx = current_context_id();
     if (kept.dev != dev || kept.ctx != ctx || ctx == 0) {
         for (int c = 1; c <= 8; ++c) {
-            e = resident_clusters(reinterpret_cast<const void *>(k_outer_tc<false>), kOutThreads, c, kOutSmem, &kept.clusters[c]);
+            e = resident_clusters(reinterpret_cast<const void *>(k_outer_tc<false, false>), kOutThreads, c, kOutSmem, &kept.clusters[c]);
             if (e != cudaSuccess) return e;
         }
         kept.dev = dev;
@@ -1217,7 +1239,7 @@ size_t act8_grads_tc_workspace_bytes(int64_t M, int64_t n, int r) {
 
 cudaError_t launch_act8_grads_tc(const int8_t *codes, const uint16_t *absmax, const uint16_t *gh, int64_t M, int64_t n,
                                  int64_t k, const uint16_t *A, const uint16_t *B, int r, float s,
-                                 const DropoutArgs &drop, float *grad_A, float *grad_B, void *ws, cudaStream_t st) {
+                                 const DropoutArgs &drop, float *grad_A, float *grad_B, void *ws, cudaStream_t st, bool give_up) {
     cudaError_t e = cudaSuccess;
     TcArgs p{absmax, M, n, k, r, 0, 0, 0, 0, false, s * (128.0f / 127.0f), grad_A, grad_B, static_cast<uint16_t *>(ws), nullptr, drop};
     char *at = static_cast<char *>(ws) + mid_bytes(M, r);
@@ -1266,7 +1288,7 @@ cudaError_t launch_act8_grads_tc(const int8_t *codes, const uint16_t *absmax, co
             return cudaErrorInvalidValue;
         const auto down = masked ? (p.rp > 32 ? k_down_tc<true, 4> : k_down_tc<true, 2>)
                                  : (p.rp > 32 ? k_down_tc<false, 4> : k_down_tc<false, 2>);
-        const auto outer = masked ? k_outer_tc<true> : k_outer_tc<false>;
+        const auto outer = give_up ? k_outer_tc<true, true> : masked ? k_outer_tc<true, false> : k_outer_tc<false, false>;
         const auto grid = [](int64_t n, int c, unsigned y) { return dim3(static_cast<unsigned>(n * c), y, 1); };
         e = launch_clusters(down, grid(tok, rd, 2), kDownThreads, kDownSmem, rd, tm_gh, tm_codes, tm_A, tm_B, p, st);
         p.tile0 = 0;

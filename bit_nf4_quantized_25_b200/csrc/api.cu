@@ -617,9 +617,10 @@ qn_status qlora_lora_grads_act8_workspace_size(int64_t M, int64_t n_out, int r, 
     return QN_OK;
 }
 
-qn_status qlora_lora_grads_act8(const qn_act8 *x, const void *grad_h, int64_t n_out, const void *A, const void *B,
-                                int r, float alpha, const qn_lora_dropout *dropout, float *grad_A, float *grad_B,
-                                void *ws, size_t ws_bytes, void *stream) {
+// give_up: the self-test's call.
+static qn_status grads_act8(const qn_act8 *x, const void *grad_h, int64_t n_out, const void *A, const void *B, int r,
+                            float alpha, const qn_lora_dropout *dropout, float *grad_A, float *grad_B, void *ws,
+                            size_t ws_bytes, void *stream, bool give_up) {
     qn_status s = check_act8(x, "x");
     if (s != QN_OK) return s;
     const int64_t M = x->rows, k = x->cols;
@@ -659,10 +660,29 @@ qn_status qlora_lora_grads_act8(const qn_act8 *x, const void *grad_h, int64_t n_
         if (e == cudaSuccess && b_bytes) e = cudaMemsetAsync(grad_B, 0, 4 * b_bytes, st);
         return cuda_status(e, "qlora_lora_grads_act8");
     }
+    if (give_up)
+        return cuda_status(launch_act8_grads_tc(x->codes, x->absmax, static_cast<const uint16_t *>(grad_h), M, n_out, k,
+                                                static_cast<const uint16_t *>(A), static_cast<const uint16_t *>(B), r, sc,
+                                                drop, grad_A, grad_B, ws, st, true),
+                           "qn_selftest_grads_give_up");
     return cuda_status(launch_act8_grads(x->codes, x->absmax, static_cast<const uint16_t *>(grad_h), M, n_out, k,
                                          static_cast<const uint16_t *>(A), static_cast<const uint16_t *>(B), r, sc,
                                          drop, grad_A, grad_B, ws, st),
                        "qlora_lora_grads_act8");
+}
+
+qn_status qlora_lora_grads_act8(const qn_act8 *x, const void *grad_h, int64_t n_out, const void *A, const void *B,
+                                int r, float alpha, const qn_lora_dropout *dropout, float *grad_A, float *grad_B,
+                                void *ws, size_t ws_bytes, void *stream) {
+    return grads_act8(x, grad_h, n_out, A, B, r, alpha, dropout, grad_A, grad_B, ws, ws_bytes, stream, false);
+}
+
+qn_status qn_selftest_grads_give_up(const qn_act8 *x, const void *grad_h, int64_t n_out, const void *A, const void *B,
+                                    int r, float alpha, const qn_lora_dropout *dropout, float *grad_A, float *grad_B,
+                                    void *ws, size_t ws_bytes, void *stream) {
+    if (x && x->rows <= 1024) return fail(QN_ESHAPE, "the self-test wants more than 1024 tokens, has %lld", (long long)x->rows);
+    if (!dropout || !(dropout->p > 0.0f)) return fail(QN_EINVAL, "the self-test wants a dropout");
+    return grads_act8(x, grad_h, n_out, A, B, r, alpha, dropout, grad_A, grad_B, ws, ws_bytes, stream, true);
 }
 
 // ------------------------------------------------- 4-bit integers with group scales

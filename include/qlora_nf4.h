@@ -389,6 +389,16 @@ qn_status qlora_lora_grads_act8(const qn_act8 *x, const void *grad_h, int64_t n_
                                 int r, float alpha, const qn_lora_dropout *dropout, float *grad_A,
                                 float *grad_B, void *ws, size_t ws_bytes, void *stream);
 
+/* qn_selftest_grads_give_up -- a check of that: qlora_lora_grads_act8 with dropout on more
+ * than 1024 tokens in which warps give up from the middle of the codes' steps on, so that
+ * the waits on them run out, within milliseconds. grad_A comes out NaN, grad_B as ever;
+ * nothing faults or hangs. No counterpart on the pages: it exists to test that failure path.
+ * Arguments and errors as qlora_lora_grads_act8; QN_EINVAL without a dropout, QN_ESHAPE for
+ * 1024 tokens or fewer. */
+qn_status qn_selftest_grads_give_up(const qn_act8 *x, const void *grad_h, int64_t n_out, const void *A, const void *B,
+                                    int r, float alpha, const qn_lora_dropout *dropout, float *grad_A, float *grad_B,
+                                    void *ws, size_t ws_bytes, void *stream);
+
 /* swiglu_act8_fwd -- the activation of the MLP, y = silu(gate) * up, keeping gate and
  * up in 8 bits:
  *   y = bf16_rn(g sigma(g) u), sigma(g) = 1 / (1 + exp(-g)), in fp32 from the bf16 gate

@@ -1,5 +1,5 @@
 """The 8-bit activations and the 4-bit integer weights on the GPU where their other tests do not reach: weights that are not
-finite, gates far below zero. Compared with 64-bit forms (lowbit_ref)."""
+finite, gates far below zero, waits that run out. Compared with 64-bit forms (lowbit_ref)."""
 import pytest
 import torch
 
@@ -10,7 +10,7 @@ if not torch.cuda.is_available():
 
 import lowbit_ref as ref
 from bit_nf4_quantized_25_b200 import binding as qb
-from test_lowbit_gpu import BF, DEV, TINY, rand, within
+from test_lowbit_gpu import BF, DEV, TINY, grad_inputs, rand, within
 
 
 # ------------------------------------------------------------------- 4-bit integers
@@ -79,3 +79,18 @@ def test_swiglu_of_gates_far_below_zero(scale):
     top = want.abs().reshape(4, -1, 64).amax(-1, keepdim=True).expand(-1, -1, 64).reshape(want.shape)
     rounding = top * (ref.HALF_STEP + 1.01 * eta) + few(g, u) + TINY
     within(ref.act8_values(y8.codes, y8.absmax), want, rounding + top * 1.02 / 254.0, "y8")
+
+
+# ------------------------------------------------------------------- adapter gradients
+
+@pytest.mark.parametrize("M,n,k,r", [(1100, 264, 320, 16), (1100, 264, 192, 64), (4100, 520, 64 * 21, 40)])
+def test_grads_of_a_call_that_gives_its_waits_up_are_nan_and_the_next_call_runs(M, n, k, r):
+    x8, gh, A, B = grad_inputs(M, n, k, r)
+    drop = (0.1, 3, 1)
+    want = qb.qlora_lora_grads_act8(x8, gh, A, B, 16.0, dropout=drop)
+    for _ in range(2):
+        ga, gb = qb.selftest_grads_give_up(x8, gh, A, B, 16.0, drop)
+        torch.cuda.synchronize()
+        assert bool(ga.isnan().all()) and torch.equal(gb, want[1])
+        again = qb.qlora_lora_grads_act8(x8, gh, A, B, 16.0, dropout=drop)
+        assert all(torch.equal(a, b) for a, b in zip(again, want))
