@@ -71,7 +71,13 @@ def build_marshal(force: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    """Both; the library first, whose C ABI needs neither g++ nor torch's headers."""
+    lib = build_library(force, verbose)
     build_marshal(force)
+    return lib
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     nvcc = _nvcc()
