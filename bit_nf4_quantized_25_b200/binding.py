@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 import functools
+import importlib.util
 import os
 import threading
 
@@ -16,7 +17,6 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libqlora_nf4.so")
-MARSHAL_PATH = os.path.join(_PKG, "_marshal.so")
 
 QN_OK, QN_EINVAL, QN_ESHAPE, QN_EALIGN, QN_ECUDA, QN_EWORKSPACE, QN_ETIMEOUT = range(7)
 BLOCK, GROUP, MAX_RANK = 64, 256, 256
@@ -483,9 +483,13 @@ def _native():
     global _marshal
     if _marshal is None:
         lib = load()
-        if not os.path.exists(MARSHAL_PATH):
-            raise RuntimeError(f"{MARSHAL_PATH} is missing: build it with `python -m bit_nf4_quantized_25_b200.build`")
-        from . import _marshal as m
+        from .build import marshal_path
+        path = marshal_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with `python -m bit_nf4_quantized_25_b200.build`")
+        spec = importlib.util.spec_from_file_location(__package__ + "._marshal", path)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
         m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
             lib.act8_quantize, lib.act8_dequantize, lib.qlora_lora_grads_act8_workspace_size, lib.qlora_lora_grads_act8,
             lib.swiglu_act8_fwd, lib.swiglu_act8_bwd, lib.int4_quantize, lib.int4_dequantize, lib.int4_linear_fwd)))

@@ -1,8 +1,8 @@
-"""Build the sm_100a shared library ``libqlora_nf4.so`` in-tree with nvcc, and ``_marshal.so`` with g++.
+"""Build the sm_100a shared library ``libqlora_nf4.so`` in-tree with nvcc, and ``_marshal.*.so`` with g++.
 
 Every ``csrc/*.cu`` file is compiled for ``-gencode arch=compute_100a,code=sm_100a``
 (parallel object builds, then one link). ``csrc/marshal.cpp`` is a Python extension module over
-torch's headers. Run ``python -m bit_nf4_quantized_25_b200.build``.
+torch's headers, one file for each Python, torch and C++ ABI that it is built against. Run ``python -m bit_nf4_quantized_25_b200.build``.
 """
 from __future__ import annotations
 
@@ -18,7 +18,6 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libqlora_nf4.so")
-MARSHAL = os.path.join(PKG, "_marshal.so")
 MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
 OBJ = os.path.join(ROOT, "_build")
 
@@ -50,24 +49,32 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def marshal_path() -> str:
+    """The extension module of this Python and this torch: built against another, it must not be loaded."""
+    import torch
+    return os.path.join(PKG, f"_marshal.{sys.implementation.cache_tag}-torch{torch.__version__}-"
+                             f"abi{int(torch.compiled_with_cxx11_abi())}.so")
+
+
 def build_marshal(force: bool = False) -> str:
+    out = marshal_path()
     newest = max(os.path.getmtime(p) for p in (MARSHAL_SRC, os.path.join(ROOT, "include", "qlora_nf4.h")))
-    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= newest:
-        return MARSHAL
+    if not force and os.path.exists(out) and os.path.getmtime(out) >= newest:
+        return out
     import torch
     home = os.path.dirname(torch.__file__)
     include = [os.path.join(ROOT, "include"), os.path.join(home, "include"),
                os.path.join(home, "include", "torch", "csrc", "api", "include"),
                os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"), sysconfig.get_paths()["include"]]
-    tmp = MARSHAL + f".tmp{os.getpid()}"
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+    tmp = out + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
            *(f"-I{d}" for d in include), MARSHAL_SRC, "-o", tmp, f"-L{os.path.join(home, 'lib')}",
            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {MARSHAL_SRC}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, MARSHAL)
-    return MARSHAL
+    os.replace(tmp, out)
+    return out
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

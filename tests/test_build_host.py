@@ -4,6 +4,7 @@ import subprocess
 import types
 
 import pytest
+import torch
 
 from bit_nf4_quantized_25_b200 import build as b
 
@@ -40,3 +41,27 @@ def test_the_library_is_built_where_the_extension_module_cannot_be(compilers):
     compilers.broken.clear()
     compilers.ran.clear()
     assert b.build() == b.LIB and compilers.ran == ["g++"]  # the library is up to date
+
+
+def test_the_extension_module_is_built_anew_for_another_torch(compilers, monkeypatch):
+    first = b.build_marshal()
+    assert b.build_marshal() == first and compilers.ran == ["g++"]
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    second = b.build_marshal()
+    assert second != first and os.path.exists(second) and compilers.ran == ["g++"] * 2
+
+
+def test_a_module_of_another_torch_is_not_loaded(monkeypatch):
+    from bit_nf4_quantized_25_b200 import binding as qb
+    b.build()
+    monkeypatch.setattr(qb, "_marshal", None)
+    assert qb._native().__file__ == b.marshal_path()
+    names = {os.path.basename(b.marshal_path())}
+    for attribute, value in (("__version__", "0.0.1"), ("compiled_with_cxx11_abi", lambda: not torch._C._GLIBCXX_USE_CXX11_ABI)):
+        with monkeypatch.context() as m:
+            m.setattr(torch, attribute, value)
+            names.add(os.path.basename(b.marshal_path()))
+            m.setattr(qb, "_marshal", None)
+            with pytest.raises(RuntimeError, match="missing"):
+                qb._native()
+    assert len(names) == 3
