@@ -12,6 +12,7 @@ import functools
 import importlib.util
 import os
 import threading
+import warnings
 
 import torch
 
@@ -477,16 +478,27 @@ def qlora_lora_grads(x: torch.Tensor, grad_h: torch.Tensor, A: torch.Tensor, B: 
 _marshal = None
 
 
+class _NoMarshal:
+    """In place of the compiled marshalling: every call takes the general way."""
+
+    def __getattr__(self, name):
+        return lambda *operands: None
+
+
 def _native():
     """The compiled marshalling of the plain calls (csrc/marshal.cpp): new results, current stream. A call of it gives the
-    results, a status, or None when the operands need the general way below."""
+    results, a status, or None when the operands need the general way below, which does the same through the same library
+    and takes the host a few microseconds more."""
     global _marshal
     if _marshal is None:
         lib = load()
         from .build import marshal_path
         path = marshal_path()
         if not os.path.exists(path):
-            raise RuntimeError(f"{path} is missing: build it with `python -m bit_nf4_quantized_25_b200.build`")
+            warnings.warn(f"{path} is missing, calls take longer on the host: build it with "
+                          "`python -m bit_nf4_quantized_25_b200.build`", RuntimeWarning, stacklevel=3)
+            _marshal = _NoMarshal()
+            return _marshal
         spec = importlib.util.spec_from_file_location(__package__ + "._marshal", path)
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)

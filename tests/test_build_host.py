@@ -62,6 +62,17 @@ def test_a_module_of_another_torch_is_not_loaded(monkeypatch):
             m.setattr(torch, attribute, value)
             names.add(os.path.basename(b.marshal_path()))
             m.setattr(qb, "_marshal", None)
-            with pytest.raises(RuntimeError, match="missing"):
-                qb._native()
+            with pytest.warns(RuntimeWarning, match="missing"):
+                assert isinstance(qb._native(), qb._NoMarshal)
     assert len(names) == 3
+
+
+def test_calls_take_the_general_way_without_the_extension_module(monkeypatch, tmp_path):
+    from bit_nf4_quantized_25_b200 import binding as qb
+    b.build()
+    monkeypatch.setattr(qb, "_marshal", None)
+    monkeypatch.setattr(b, "PKG", str(tmp_path))
+    x = torch.zeros(2, 64, dtype=torch.bfloat16)
+    with pytest.warns(RuntimeWarning, match="bit_nf4_quantized_25_b200.build"), \
+            pytest.raises(ValueError, match="not on a CUDA device"):  # the general way's answer
+        qb.act8_quantize(x)

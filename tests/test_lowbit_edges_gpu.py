@@ -1,5 +1,6 @@
 """The 8-bit activations and the 4-bit integer weights on the GPU where their other tests do not reach: weights that are not
-finite, gates far below zero, waits that run out. Compared with 64-bit forms (lowbit_ref)."""
+finite, gates far below zero, waits that run out, calls without the compiled
+marshalling. Compared with 64-bit forms (lowbit_ref)."""
 import pytest
 import torch
 
@@ -94,3 +95,22 @@ def test_grads_of_a_call_that_gives_its_waits_up_are_nan_and_the_next_call_runs(
         assert bool(ga.isnan().all()) and torch.equal(gb, want[1])
         again = qb.qlora_lora_grads_act8(x8, gh, A, B, 16.0, dropout=drop)
         assert all(torch.equal(a, b) for a, b in zip(again, want))
+
+
+# ------------------------------------------------------------------- marshalling
+
+def test_calls_without_the_compiled_marshalling_give_the_same(monkeypatch):
+    x, up, dy, W = rand(6, 320, seed=1), rand(6, 320, seed=2), rand(6, 320, seed=3), rand(24, 320, std=0.02, seed=4)
+    A, B = rand(8, 320, seed=5), rand(320, 8, seed=6)
+
+    def step():
+        a = qb.act8_quantize(x)
+        y, g8, u8 = qb.swiglu_act8_fwd(x, up)
+        gg, gu, y8 = qb.swiglu_act8_bwd(g8, u8, dy)
+        w = qb.int4_quantize(W, group=64)
+        return (a.codes, a.absmax, qb.act8_dequantize(a), y, g8.codes, u8.absmax, gg, gu, y8.codes, w.codes, w.scale,
+                w.zero_point, qb.int4_dequantize(w), qb.int4_linear_fwd(w, x), *qb.qlora_lora_grads_act8(a, up, A, B, 8.0))
+
+    want = step()
+    monkeypatch.setattr(qb, "_marshal", qb._NoMarshal())
+    assert all(torch.equal(a, b) for a, b in zip(step(), want))
