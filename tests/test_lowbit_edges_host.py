@@ -34,3 +34,15 @@ def test_the_give_up_self_test_refuses_what_it_does_not_take(qb):
     assert call(gh=None) == EINVAL and call(gh=P(0x40000002)) == EALIGN
     assert call(rank=0) == EINVAL and call(size=size - 1) == EWORKSPACE
     assert lib.qn_launch_count(0) == before
+
+
+def test_the_package_offers_the_size_of_every_workspace_that_a_call_takes(qb):
+    import inspect
+
+    import bit_nf4_quantized_25_b200 as package
+    takes = {name for name in package.__all__ if "workspace" in inspect.signature(getattr(package, name)).parameters}
+    assert takes == {"nf4_quantize", "qlora_linear_fwd", "qlora_linear_bwd_x", "qlora_lora_grads", "qlora_lora_grads_act8"}
+    assert package.quantize_workspace_size(64, 128) > 0 and package.linear_workspace_size(3, 64, 128, 8) > 0
+    assert package.lora_grads_workspace_size(40, 8) > 0
+    assert package.lora_grads_act8_workspace_size(1100, 97, 8) > package.lora_grads_act8_workspace_size(1100, 96, 8) > 0
+    assert set(package.__all__) <= set(dir(package)) and len(package.__all__) == len(set(package.__all__))
