@@ -13,8 +13,8 @@
 // of 64, so blocks never straddle rows and the tensor is walked as one flat array. Each thread takes
 // kUnroll words, all loaded before the first is used.
 //
-// Measured at 4096 x 11008: quantise 22.8 us, read back 22.7 us (6.0 TB/s, 0.93 of the measured HBM rate), SwiGLU forward
-// 60.3 us (6.0 TB/s), backward 71.3 us (5.75 TB/s, 0.89; its issue slots are 82 % busy).
+// Measured at 4096 x 11008, on three sets of buffers in turn: quantise 22.7 us, read back 22.6 us (6.0 TB/s, 0.93 of the
+// measured HBM rate), SwiGLU forward 60.5 us (6.0 TB/s), backward 72.7 us (5.6 TB/s, 0.87; its issue slots are 82 % busy).
 #include "act8.cuh"
 #include "act8.h"
 #include "dependent.cuh"

@@ -21,8 +21,10 @@
 //
 // CTAs split the rank too, in blocks of 8 or 16 columns j.
 //
-// Measured: 256 x 256, 8 tokens, rank 4 5.8 us, 4096 x 4096, 16 tokens, rank 16 8.0 us; the latency of two kernels, each
-// of loads, a few MMAs and sums across a cluster, bounds them. 28672 x 8192, 120 tokens, rank 64 39.6 us.
+// Measured: 256 x 256, 8 tokens, rank 4 5.4 us, 4096 x 4096, 16 tokens, rank 16 7.8 to 9.9 us; the latency of two kernels, each
+// of loads, a few MMAs and sums across a cluster, bounds them. 28672 x 8192, 120 tokens, rank 64 41 to 47 us, for 3.4 us of
+// bytes: each block of 16 columns of the rank loads and converts x and grad_h anew. With dropout 14.8 us at 16 tokens and
+// 74 us at 120: the mask is drawn anew for each block of columns, too.
 #include "act8.cuh"
 #include "act8.h"
 #include "dropout.cuh"

@@ -20,14 +20,19 @@
 //               is read with its M index contiguous, as it lies. A cluster splits the tokens. It walks them backwards:
 //               what the first kernel read last is still in L2.
 //
+// The 23 warps of k_outer_tc leave 80 registers a thread; it spills 128 B (132 B with dropout), whose cost was not timed.
+//
 // Warp 0 issues the TMA loads, warp 1 the MMAs, one warp brings absmaxes, the others convert codes, drain accumulators and
 // run the epilogue. Every wait on an mbarrier is bounded; a CTA whose wait runs out drains what it issued and its results are
 // NaN. A warp gives up as a whole, since what follows a wait wants all its lanes, and the warps of a group that meet at
 // a barrier in every step leave together (see group_all).
 //
-// Measured at 4096 tokens: 4096 x 4096, rank 16 40 us (the bytes once: 8 us), 28672 x 8192, rank 64 128 us (44 us). A step
-// of k_outer_tc takes 0.42 us of x (conversion: ldmatrix, products and tcgen05.st of one step are a chain of 1.4 us, in
-// four groups) and of grad_h (32 KB); to that come 5 us until the first step of x and 5 us of epilogue.
+// Measured at 4096 tokens: 4096 x 4096, rank 16 39 us (the bytes once: 8 us), 28672 x 8192, rank 64 128 to 150 us (44 us; sets
+// of buffers of the same sizes differ by that much, each repeats to 5 %). A step of k_outer_tc takes 0.42 us of x (conversion:
+// ldmatrix, products and tcgen05.st of one step are a chain of 1.4 us, in four groups; two terms of each code, as a
+// goes in with x; with u instead, scaled for each 64 columns, is not built) and of grad_h (32 KB); to that come 5 us until the first
+// step of x and 5 us of epilogue. Each 64 columns of the rank are a pass of their own: rank 128 111 us and 256 to 293 us. Dropout:
+// 193 us and 530 us; both kernels draw the mask, in the warps that convert.
 #include <cudaTypedefs.h>
 
 #include "act8.cuh"

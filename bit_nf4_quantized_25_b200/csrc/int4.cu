@@ -13,8 +13,9 @@
 // which share its minimum and maximum by shuffles. k % group == 0, so groups do not straddle rows and
 // the matrix is walked as one flat array.
 //
-// Measured at 28672 x 8192, groups of 64 with zero points: quantise 103.8 us (5.8 TB/s, 0.89 of the measured HBM rate),
-// read back 99.8 us (6.0 TB/s, 0.93).
+// Measured at 28672 x 8192, groups of 64, on three sets of buffers in turn: with zero points quantise 110 to 113 us (5.3 to
+// 5.4 TB/s, 0.83 of the measured HBM rate), read back 100.5 us (6.0 TB/s, 0.92); without quantise 96.7 to 98.6 us (6.1 TB/s, 0.94),
+// read back 93.3 us.
 #include "common.cuh"
 #include "dependent.cuh"
 #include "int4.h"
@@ -55,7 +56,7 @@ __device__ __forceinline__ void range(const uint4 &v, float &hi, float &below) {
 
 // Scale, zero point and codes of a lane's 8 weights in a group with this range.
 //
-// The quotient w / s is taken as w inv with inv = (1 + 2^-17) / s to 2^-21 of itself: w and s have 8-bit
+// The quotient w / s is taken as w inv with inv = (1 + 2^-16) / s to 2^-21 of itself: w and s have 8-bit
 // significands, so a quotient that is not a half is at least 1 / 512 of a unit away from one, and one
 // that is a half is raised above it by more than the error of inv; at up to 16 units the raise is
 // below 2^-12. An fma onto 1.5 * 2^23 + z then gives round(w / s) + z with halves away from zero.
@@ -85,7 +86,7 @@ __device__ __noinline__ uint4 encode_any(uint4 v, float hi, float below) {  // c
 }
 
 // The same for ordinary ranges, in a third of the instructions (with encode_any for all the kernel was bound by issuing them:
-// 28672 x 8192 took 131 us). span / 15 (7) is the product with the reciprocal and one correction by its remainder, which
+// 28672 x 8192 took 131 us instead of 104). span / 15 (7) is the product with the reciprocal and one correction by its remainder, which
 // rounds as the division does (Markstein's theorem; checked for every significand). s is then span / 15 (7) to 2^-8.9 of itself, so
 // w / s is above -z - 1/2 and, without zero points, within 7.1: only w / s + z with zero points can come out above 15, by 1.
 template <bool kZero>

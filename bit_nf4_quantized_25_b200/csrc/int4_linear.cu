@@ -19,11 +19,13 @@
 // warp has kSlots steps of its weights in flight, in a ring of its own: asynchronous copies, since loads to registers
 // that are waited for one by one end up waiting for the youngest. The parts' sums meet in shared memory.
 //
-// Measured, with zero points: 4096 x 4096 (group 128) 1 token 6.7 us; 8192 x 28672 (128) 1, 8 and 16 tokens 34.5, 41.3 and
-// 59.1 us (3.6, 3.0 and 2.1 TB/s); 11008 x 4096 (32) 5 tokens 13.9 us. Three quarters of the warps' time goes by in the
-// loop, 190 instructions of a warp for 16 rows x 128 k at 16 tokens, and no pipe is busy for a third of it: waits between
-// dependent instructions bound it, four warps to a scheduler. x of 16 tokens leaves no room for more, and 120 of 148 SMs hold
-// the clusters of 8 that it needs. Small calls are start-up, the copy of x and the sums across CTAs.
+// Measured, with zero points: 4096 x 4096 (group 128) 1 token 6.5 to 6.9 us; 8192 x 28672 (128) 1, 8 and 16 tokens 34.3, 41.6
+// and 58.7 us (3.6, 3.0 and 2.1 TB/s), 32 and 64 tokens 117 and 233 us (a pass over the weights for each 16); 11008 x 4096 (32)
+// 5 tokens 14.7 us. At 16 tokens three quarters of the warps' time goes by in the loop, 190 instructions of a warp for 16 rows x
+// 128 k, and no pipe is busy for a third of it: waits between dependent instructions bound it, four warps to a scheduler. x of 16
+// tokens leaves no room for more, and 120 of 148 SMs hold the clusters of 8 that it needs. One token runs under the same plan, and
+// x has eight columns of shared memory for it: a choice (see plan), not a limit of its own. Small calls are start-up, the copy of x
+// and the sums across CTAs.
 #include "common.cuh"
 #include "dependent.cuh"
 #include "host_cache.h"
