@@ -58,7 +58,7 @@ __device__ __forceinline__ float reciprocal(float v) {  // of 1 .. 2^126, by the
 
 // sigma(g) = e / (1 + e) below 0 and 1 / (1 + e) from 0 on, with e = exp(-|g|) <= 1, so that no gate leads out of the
 // reciprocal's range. By the hardware exponential, of a rounded argument, and reciprocal it is off by at most
-// (3 + 1.2 |g|) 2^-23 of itself, below 2^-16 in all of fp32's normal range and far below the bf16 rounding of the results;
+// (4 + 1.2 |g|) 2^-23 of itself, below 2^-16 in all of fp32's normal range and far below the bf16 rounding of the results;
 // below 2^-126 it is a multiple of 2^-149.
 __device__ __forceinline__ float sigmoid(float g) {
     const float e = __expf(-fabsf(g));

@@ -402,7 +402,7 @@ qn_status qn_selftest_grads_give_up(const qn_act8 *x, const void *grad_h, int64_
 /* swiglu_act8_fwd -- the activation of the MLP, y = silu(gate) * up, keeping gate and
  * up in 8 bits:
  *   y = bf16_rn(g sigma(g) u), sigma(g) = 1 / (1 + exp(-g)), in fp32 from the bf16 gate
- *   and up; gate8, up8: their 8-bit forms. sigma is off by at most (3 + 1.2 |g|) 2^-23 of
+ *   and up; gate8, up8: their 8-bit forms. sigma is off by at most (4 + 1.2 |g|) 2^-23 of
  *   itself, and by a step of fp32 (2^-149) where it is below 2^-126 (g below -87.3).
  * gate, up, y : rows x cols bf16 with gate8's rows and cols; up8 has the same. No
  * output may overlap another output or an input.
